@@ -64,6 +64,8 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_ACT_BF16 = 0, MOE_ACT_FP16 = 1 } moe_act_dtype;
+/* Storage types of moe_add_rms_norm, moe_select_experts and moe_linear (the first two as above). */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 } moe_dtype;
 typedef enum { MOE_W_MXFP4 = 0, MOE_W_FP16 = 1, MOE_W_INT4_G32 = 2, MOE_W_NVFP4 = 3 } moe_w_format;
 
 /* One projection of every expert: logical [n_experts][N][K], K contiguous within a row [MX].
@@ -152,6 +154,58 @@ moe_status moe_route_sigmoid(const void *x, moe_act_dtype x_dtype, int T, int H,
                              const float *selection_bias, int E, int top_k, int n_shared,
                              float routed_scale, float shared_weight, int32_t *ids, float *weights,
                              float *scores, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Routing by a rule: scores, a balance bias, groups of experts, top-k (group-limited routing; not on
+ * the pages).  Per token with logits L[e], e < E, and b = selection_bias (0 without one):
+ *   scores    s[e] = 1 / (1 + e^-L[e]) (SIGMOID), or softmax(L) over the experts with finite L (SOFTMAX);
+ *   keys      s[e] + b[e]: the bias moves the choice only, never a weight;
+ *   available an expert with a finite logit and a finite bias.  A logit of -inf masks an expert for a
+ *             token, a bias of -inf for all tokens (NaN and +inf mask too);
+ *   groups    group g holds experts g * E/n_groups .. (g+1) * E/n_groups - 1.  Its rank is the sum of its
+ *             two largest available keys (TOP2; the one key where it has only one) or the largest (MAX).
+ *             The topk_groups groups of the largest ranks stay, the lowest index first on ties;
+ *   slots     j = 0 .. top_k-1 hold the available experts of those groups by (key descending, index
+ *             ascending), weights[t,j] = routed_scale * s_j, divided by the sum of the selected s if
+ *             renormalise.  Where fewer than top_k are left, the other slots get id -1 and weight 0 (as
+ *             moe_pad_rows marks them: moe_bucket drops them).  A sum of scores that underflows fp32 gives
+ *             weights of 0;
+ *   shared    slots top_k .. top_k+n_shared-1 hold experts E .. E+n_shared-1 with weight shared_weight.
+ * The choice is that of the keys in 64 bits, also where two keys or ranks are closer than fp32 can
+ * tell.  It is a function of the logits; ids of moe_route_grouped also depend on the logits' own fp32
+ * rounding, as moe_route's do.
+ * The struct is a HOST struct; selection_bias is a device pointer to [E] fp32, or NULL. */
+#define MOE_MAX_GROUPS 64
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+typedef enum { MOE_GROUP_TOP2 = 0, MOE_GROUP_MAX = 1 } moe_group_score;
+typedef struct {
+  moe_score score;
+  int top_k, n_shared;
+  int n_groups, topk_groups;   /* 1 and 1: no groups */
+  moe_group_score group_score;
+  int renormalise;
+  float routed_scale, shared_weight;
+  const float *selection_bias;
+} moe_route_rule;
+
+/* moe_select_experts -- the rule on given logits.
+ *   logits  [T] rows of E values (bf16, fp16 or fp32), row_stride values apart (>= E), aligned to a value
+ *   ids     [T][top_k+n_shared] int32 out;  weights [T][top_k+n_shared] fp32 out
+ *   scores  [T][E] fp32 out (s; 0 for an expert whose logit is not finite), or NULL
+ * One launch, no workspace.
+ * Errors: NULL, SHAPE (T<0, E<1, E>MOE_MAX_EXPERTS, n_shared<0, row_stride<E, n_groups outside
+ * [1, MOE_MAX_GROUPS] or not a divisor of E, topk_groups outside [1, n_groups], a routed_scale or
+ * shared_weight that is not finite), TOPK (top_k < 1 or beyond topk_groups * E/n_groups, or
+ * top_k+n_shared > MOE_MAX_SLOTS_PER_TOKEN), DTYPE, ALIGN, HIP. */
+moe_status moe_select_experts(const void *logits, moe_dtype logits_dtype, int64_t row_stride, int T, int E,
+                              const moe_route_rule *rule, int32_t *ids, float *weights, float *scores,
+                              void *stream);
+/* moe_route_grouped -- the rule on L = x w_router^T (fp32, as moe_route computes it).  x, w_router, workspace
+ * (moe_route_workspace_bytes(T, H, E) bytes) as for moe_route, the rest as above.
+ * Errors: as both calls. */
+moe_status moe_route_grouped(const void *x, moe_act_dtype x_dtype, int T, int H, const float *w_router, int E,
+                             const moe_route_rule *rule, int32_t *ids, float *weights, float *scores,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Fixed row shapes [C32] (Cascadia Sec. 3.2: a call's rows are run at one of the row shapes the
@@ -367,6 +421,67 @@ moe_status moe_expert_ffn_mx(const void *x, moe_act_dtype x_dtype, int T, int k_
  * ([T*k_total][inter/32]).  offsets is a host array of 4.  Errors: NULL, SHAPE, DTYPE. */
 moe_status moe_expert_ffn_mx_workspace_layout(int T, int k_total, const moe_expert_weights *W,
                                               moe_mx_format fmt, size_t *offsets);
+
+/* moe_expert_ffn_mx_codes -- moe_expert_ffn_mx on an x that is quantised already (by moe_mx_quantize, or by
+ * moe_add_rms_norm): x_codes [T] packed rows of `hidden` values (16-byte aligned), x_scales [T][hidden/32]
+ * E8M0 (4-byte aligned).  The same results, bit for bit, as moe_expert_ffn_mx on the x they came from, without
+ * its quantisation launch.  workspace: moe_expert_ffn_mx_workspace_bytes (its x part stays unused).
+ * Errors: as moe_expert_ffn_mx. */
+moe_status moe_expert_ffn_mx_codes(const uint8_t *x_codes, const uint8_t *x_scales, int T, int k_total,
+                                   const moe_expert_weights *W, moe_mx_format fmt, const int32_t *offsets,
+                                   const int32_t *sorted_slot, float *y_slots, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_add_rms_norm -- the residual addition and root-mean-square norm in front of a layer (not on the pages).
+ * Per row t, in fp32 with one rounding at each output:
+ *   s = x[t,:] + residual[t,:]   (s = x[t,:] without a residual)
+ *   residual_out[t,:] = s
+ *   y[t,h] = s[h] * weight[h] / sqrt(sum_h s[h]^2 / hidden + eps)
+ *   codes[t], scales[t] = the MX block quantisation (see MX mode) of the fp32 y before it is rounded to y_dtype;
+ *   fmt MOE_MX_FP8_E4M3 is the 8-bit output, in the layout of moe_expert_ffn_mx_codes.  y must be finite there.
+ * Types: x, residual (and residual_out), weight and y each bf16, fp16 or fp32.  x may be moe_combine's or
+ * moe_linear's fp32 output, y is what moe_route, moe_linear and moe_expert_ffn read.
+ *   x, residual, residual_out  [T] rows of `hidden` values, *_row_stride values apart (>= hidden), aligned to a
+ *       value.  residual may be NULL (then residual_out must be too); residual_out may be NULL, and may be
+ *       residual itself (same pointer and stride: the sum replaces it in place; any other overlap is an error
+ *       that is not checked)
+ *   y       [T][hidden], aligned to a value, or NULL
+ *   codes   [T] packed rows (moe_mx_row_bytes), 16-byte aligned; scales [T][hidden/32]; fmt 0: both NULL
+ * Rows of 16-byte aligned pointers and strides with hidden a multiple of 8, up to 32768, take the fast kernels.
+ * Errors: NULL (also neither y nor codes wanted, residual_out without residual), SHAPE (T<0, hidden<1, a stride
+ * below hidden, eps negative or not finite), BLOCK (codes with hidden % 32), DTYPE, ALIGN, HIP. */
+typedef struct {
+  const void *weight;  /* [hidden], aligned to a value */
+  moe_dtype weight_dtype;
+  int hidden;
+  float eps;
+} moe_norm;
+moe_status moe_add_rms_norm(const moe_norm *norm, const void *x, moe_dtype x_dtype, int64_t x_row_stride,
+                            const void *residual, moe_dtype residual_dtype, int64_t residual_row_stride, int T,
+                            void *residual_out, int64_t residual_out_row_stride, void *y, moe_dtype y_dtype,
+                            int fmt, uint8_t *codes, uint8_t *scales, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * moe_linear -- a product with 4-bit weights (an attention projection, a dense FFN's matrix, an output head):
+ *   y[t,n] = sum_k x[t,k] * W[n,k] + bias[n]   (exact decoded weights and products, fp32 sums, one rounding)
+ * W: one matrix [n_out][k_in] in MXFP4, INT4_G32 or NVFP4 (moe_proj; its expert strides are not used, an NVFP4
+ * tensor_scale is one value).  k_in a positive multiple of 32, n_out any.  x bf16, as for every 4-bit format.
+ *   x    [T] rows of k_in values, x_row_stride values apart (>= k_in, a multiple of 8), 16-byte aligned
+ *   bias [n_out] fp32, or NULL
+ *   y    [T] rows of n_out values (bf16, fp16 or fp32), y_row_stride values apart (>= n_out), aligned to a value
+ *   workspace moe_linear_workspace_bytes(T, W) bytes, 16-byte aligned (NULL if that is 0)
+ * Errors: NULL, SHAPE (also a weight row stride of 2^25 bytes or more), BLOCK, ALIGN, DTYPE (FP16 weights, x not
+ * bf16), WORKSPACE, HIP. */
+typedef struct {
+  moe_w_format fmt;
+  int n_out, k_in;
+  moe_proj w;
+} moe_linear_weights;
+size_t moe_linear_workspace_bytes(int T, const moe_linear_weights *W);
+moe_status moe_linear(const void *x, moe_act_dtype x_dtype, int64_t x_row_stride, int T,
+                      const moe_linear_weights *W, const float *bias, void *y, moe_dtype y_dtype,
+                      int64_t y_row_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
  * moe_combine -- weighted reduction [C31] with FP32 output [C32]:

@@ -10,6 +10,13 @@ present.
     b = moe_bucket(ids, n_experts)                                     # group slots by expert
     y_slots = moe_expert_ffn(x, W, b.offsets, b.sorted_slot, k_total)  # SwiGLU experts
     y = moe_combine(y_slots, w)                                        # weighted combine, fp32
+
+In front of the layer stand the projection of the attention output, the residual addition with its norm, and
+group-limited routing (MoEBlock runs them all):
+
+    a = moe_linear(attn, W_o)                                          # 4-bit weights, fp32 out
+    x, r, _, _ = moe_add_rms_norm(a, norm, residual)                   # residual stream and the layer's input
+    ids, w, _ = moe_route_grouped(x, w_router, rule)                   # scores, bias, groups, top-k
 """
 from __future__ import annotations
 
@@ -30,6 +37,10 @@ MOE_W_MXFP4, MOE_W_FP16, MOE_W_INT4_G32, MOE_W_NVFP4 = 0, 1, 2, 3
 W_FORMATS = {"mxfp4": MOE_W_MXFP4, "fp16": MOE_W_FP16, "int4g32": MOE_W_INT4_G32, "nvfp4": MOE_W_NVFP4}
 MOE_MX_FP8_E4M3, MOE_MX_FP4_E2M1, MOE_MX_FP6_E2M3 = 1, 2, 3
 MX_FORMATS = {"fp8": MOE_MX_FP8_E4M3, "fp4": MOE_MX_FP4_E2M1, "fp6": MOE_MX_FP6_E2M3}
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype
+SCORES = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORES = {"top2": 0, "max": 1}
+MOE_MAX_GROUPS = 64
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_BLOCK", 4: "MOE_ERR_ALIGN",
           5: "MOE_ERR_DTYPE", 6: "MOE_ERR_TOPK", 7: "MOE_ERR_WORKSPACE", 8: "MOE_ERR_HIP"}
@@ -52,6 +63,22 @@ class moe_proj(ctypes.Structure):
 class moe_expert_weights(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("n_experts", ctypes.c_int), ("hidden", ctypes.c_int),
                 ("inter", ctypes.c_int), ("gate", moe_proj), ("up", moe_proj), ("down", moe_proj)]
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("top_k", ctypes.c_int), ("n_shared", ctypes.c_int),
+                ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int), ("group_score", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("routed_scale", ctypes.c_float), ("shared_weight", ctypes.c_float),
+                ("selection_bias", ctypes.c_void_p)]
+
+
+class moe_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int), ("hidden", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
+class moe_linear_weights(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("n_out", ctypes.c_int), ("k_in", ctypes.c_int), ("w", moe_proj)]
 
 
 _lib = None
@@ -116,6 +143,18 @@ def lib() -> ctypes.CDLL:
                                                          ctypes.POINTER(ctypes.c_size_t)]
         L.moe_expert_ffn_mx.restype = i
         L.moe_expert_ffn_mx.argtypes = [vp, i, i, i, ctypes.POINTER(moe_expert_weights), i, vp, vp, vp, vp, st, vp]
+        L.moe_expert_ffn_mx_codes.restype = i
+        L.moe_expert_ffn_mx_codes.argtypes = [vp, vp, i, i, ctypes.POINTER(moe_expert_weights), i, vp, vp, vp, vp, st,
+                                              vp]
+        L.moe_select_experts.restype = i
+        L.moe_select_experts.argtypes = [vp, i, i64, i, i, vp, vp, vp, vp, vp]
+        L.moe_route_grouped.restype = i
+        L.moe_route_grouped.argtypes = [vp, i, i, i, vp, i, vp, vp, vp, vp, vp, st, vp]
+        L.moe_add_rms_norm.restype = i
+        L.moe_add_rms_norm.argtypes = [vp, vp, i, i64, vp, i, i64, i, vp, i64, vp, i, i, vp, vp, vp]
+        L.moe_linear_workspace_bytes.restype = st; L.moe_linear_workspace_bytes.argtypes = [i, vp]
+        L.moe_linear.restype = i
+        L.moe_linear.argtypes = [vp, i, i64, i, vp, vp, vp, i, i64, vp, st, vp]
         L.moe_stream_read.restype = i
         L.moe_stream_read.argtypes = [vp, st, vp, vp]
         _lib = L
@@ -485,6 +524,251 @@ def moe_expert_ffn_mx(x: torch.Tensor, W: ExpertWeights, fmt, offsets: torch.Ten
     return y
 
 
+def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: ExpertWeights, fmt,
+                            offsets: torch.Tensor, sorted_slot: torch.Tensor, k_total: int,
+                            out: Optional[torch.Tensor] = None, workspace=None) -> torch.Tensor:
+    """moe_expert_ffn_mx on an x given as MX codes [T][row bytes] and E8M0 scales [T][hidden/32] (uint8, as
+    moe_mx_quantize and moe_add_rms_norm write them): -> y_slots fp32."""
+    T = x_codes.shape[0]
+    dev = x_codes.device
+    f = _mx_fmt(fmt)
+    _dense("moe_expert_ffn_mx_codes: x_codes", x_codes, torch.uint8, (T, moe_mx_row_bytes(f, W.hidden)))
+    _dense("moe_expert_ffn_mx_codes: x_scales", x_scales, torch.uint8, (T, W.hidden // 32))
+    y = out if out is not None else torch.empty((T * k_total, W.hidden), dtype=torch.float32, device=dev)
+    ws = workspace if workspace is not None else _workspace(moe_expert_ffn_mx_workspace_bytes(T, k_total, W, f), dev)
+    _check(lib().moe_expert_ffn_mx_codes(_ptr(x_codes), _ptr(x_scales), T, k_total, ctypes.byref(W.c), f,
+                                         _ptr(offsets), _ptr(sorted_slot), _ptr(y), _ptr(ws),
+                                         0 if ws is None else ws.numel(), _stream(dev)), "moe_expert_ffn_mx_codes")
+    return y
+
+
+# ----------------------------------------------------------------------------------------------------
+# In front of the layer.  These calls run once per layer and token, with few microseconds of GPU time at small T:
+# the descriptions are built once, and a call passes plain integers.
+def _dense(what: str, t: torch.Tensor, dtype, shape) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _rows(what: str, t: torch.Tensor, width: int, device=None) -> int:
+    """Row stride (in values) of a [T][width] tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != width or (t.stride(1) != 1 and width > 1):
+        raise ValueError(f"{what} must be [T][{width}] with contiguous rows, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def _dtype(what: str, t: torch.Tensor) -> int:
+    d = DTYPES.get(t.dtype)
+    if d is None:
+        raise TypeError(f"{what} must be bfloat16, float16 or float32, got {t.dtype}")
+    return d
+
+
+class _on:
+    """The tensor's device made current for a call, and its current stream."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError(f"needs a GPU tensor, got one on {device}")
+        self.index = device.index
+
+    def __enter__(self) -> int:
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc) -> None:
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+class RouteRule:
+    """How experts are chosen from logits (moe_route_rule): score "softmax" or "sigmoid"; an optional fp32
+    selection_bias [E] that moves the choice only; n_groups groups of which the topk_groups best stay, ranked by
+    their two best keys ("top2") or their best ("max"); top_k experts, whose weights are renormalised or not and
+    scaled; n_shared experts after them with a fixed weight."""
+
+    def __init__(self, top_k: int, score: str = "softmax", selection_bias: Optional[torch.Tensor] = None,
+                 n_groups: int = 1, topk_groups: int = 1, group_score: str = "top2", renormalise: bool = True,
+                 routed_scale: float = 1.0, n_shared: int = 0, shared_weight: float = 1.0):
+        if selection_bias is not None:
+            _dense("RouteRule: selection_bias", selection_bias, torch.float32, (selection_bias.numel(),))
+        self.selection_bias, self.top_k, self.n_shared = selection_bias, top_k, n_shared
+        self.c = moe_route_rule(SCORES[score], top_k, n_shared, n_groups, topk_groups, GROUP_SCORES[group_score],
+                                int(bool(renormalise)), routed_scale, shared_weight,
+                                None if selection_bias is None else selection_bias.data_ptr())
+        self.at = ctypes.addressof(self.c)
+
+
+def _route_out(what: str, rule: RouteRule, T: int, E: int, dev, want_scores: bool, out):
+    b = rule.selection_bias
+    if b is not None and (b.numel() != E or b.device != dev):
+        raise ValueError(f"{what}: the selection bias has {b.numel()} values on {b.device}, expected {E} on {dev}")
+    kt = rule.top_k + rule.n_shared
+    if out is None:
+        return (torch.empty((T, kt), dtype=torch.int32, device=dev),
+                torch.empty((T, kt), dtype=torch.float32, device=dev),
+                torch.empty((T, E), dtype=torch.float32, device=dev) if want_scores else None)
+    ids, w, scores = out
+    _dense(f"{what}: ids", ids, torch.int32, (T, kt))
+    _dense(f"{what}: weights", w, torch.float32, (T, kt))
+    if scores is not None:
+        _dense(f"{what}: scores", scores, torch.float32, (T, E))
+    return out
+
+
+def moe_select_experts(logits: torch.Tensor, rule: RouteRule, want_scores: bool = False, out=None):
+    """The rule on router logits [T][E] (bf16, fp16 or fp32, contiguous rows)
+    -> (ids int32 [T][k'], weights fp32 [T][k'], scores fp32 [T][E] or None)."""
+    T, E = logits.shape
+    dev = logits.device
+    ids, w, scores = _route_out("moe_select_experts", rule, T, E, dev, want_scores, out)
+    stride = _rows("moe_select_experts: logits", logits, E)
+    with _on(dev) as stream:
+        _check(lib().moe_select_experts(logits.data_ptr(), _dtype("logits", logits), stride, T, E, rule.at,
+                                        ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
+                                        stream), "moe_select_experts")
+    return ids, w, scores
+
+
+def moe_route_grouped(x: torch.Tensor, w_router: torch.Tensor, rule: RouteRule, want_scores: bool = False, out=None,
+                      workspace=None):
+    """The rule on the logits x w_router^T -> (ids, weights, scores) as moe_select_experts."""
+    T, H = x.shape
+    E = w_router.shape[0]
+    dev = x.device
+    _dense("moe_route_grouped: x", x, x.dtype, (T, H))
+    _dense("moe_route_grouped: w_router", w_router, torch.float32, (E, H))
+    ids, w, scores = _route_out("moe_route_grouped", rule, T, E, dev, want_scores, out)
+    ws = workspace if workspace is not None else _workspace(moe_route_workspace_bytes(T, H, E), dev)
+    with _on(dev) as stream:
+        _check(lib().moe_route_grouped(x.data_ptr(), _act_dtype(x), T, H, w_router.data_ptr(), E, rule.at,
+                                       ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
+                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                                       stream), "moe_route_grouped")
+    return ids, w, scores
+
+
+class RmsNorm:
+    """Weight [hidden] (bf16, fp16 or fp32) and eps of a root-mean-square norm (moe_norm)."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-6):
+        _dense("RmsNorm: weight", weight, weight.dtype, (weight.numel(),))
+        self.weight, self.hidden = weight, weight.numel()
+        self.c = moe_norm(weight.data_ptr(), _dtype("RmsNorm: weight", weight), self.hidden, eps)
+        self.at = ctypes.addressof(self.c)
+
+
+def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Tensor] = None, mx=None,
+                     dtype: torch.dtype = torch.bfloat16, out=None):
+    """s = x + residual, y = s * weight / sqrt(mean(s^2) + eps), rows of `norm.hidden` values
+    -> (y, residual_out, codes, scales): y [T][hidden] in `dtype`; residual_out = s in the residual's type (None
+    without a residual); for mx "fp8", "fp6" or "fp4" the MX codes and scales of y as moe_mx_quantize lays them
+    out (None without).  `out` gives the four buffers; a None for y or residual_out there leaves that output
+    out, and residual_out may be residual itself."""
+    T, H = x.shape
+    dev = x.device
+    f = 0 if mx is None else _mx_fmt(mx)
+    if norm.weight.device != dev:
+        raise ValueError(f"moe_add_rms_norm: the weight is on {norm.weight.device}, x on {dev}")
+    xs = _rows("moe_add_rms_norm: x", x, norm.hidden)
+    rs = ros = rdt = 0
+    if residual is not None:
+        rs, rdt = _rows("moe_add_rms_norm: residual", residual, H, dev), _dtype("residual", residual)
+        if residual.shape[0] != T:
+            raise ValueError(f"moe_add_rms_norm: {T} rows of x, {residual.shape[0]} of the residual")
+    if out is None:
+        y = torch.empty((T, H), dtype=dtype, device=dev)
+        ro = None if residual is None else torch.empty((T, H), dtype=residual.dtype, device=dev)
+        codes = scales = None
+        if f:
+            codes = torch.empty((T, moe_mx_row_bytes(f, H)), dtype=torch.uint8, device=dev)
+            scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+    else:
+        y, ro, codes, scales = out
+        if y is not None:
+            _dense("moe_add_rms_norm: y", y, y.dtype, (T, H))
+        if f:
+            _dense("moe_add_rms_norm: codes", codes, torch.uint8, (T, moe_mx_row_bytes(f, H)))
+            _dense("moe_add_rms_norm: scales", scales, torch.uint8, (T, H // 32))
+        if ro is not None and (residual is None or ro.dtype != residual.dtype or ro.shape[0] != T):
+            raise ValueError("moe_add_rms_norm: residual_out needs a residual of its type and rows")
+    if ro is not None:
+        ros = _rows("moe_add_rms_norm: residual_out", ro, H, dev)
+    with _on(dev) as stream:
+        _check(lib().moe_add_rms_norm(norm.at, x.data_ptr(), _dtype("x", x), xs,
+                                      None if residual is None else residual.data_ptr(), rdt, rs, T,
+                                      None if ro is None else ro.data_ptr(), ros, None if y is None else y.data_ptr(),
+                                      0 if y is None else _dtype("y", y), f, None if codes is None else codes.data_ptr(),
+                                      None if scales is None else scales.data_ptr(), stream), "moe_add_rms_norm")
+    return y, ro, codes, scales
+
+
+class LinearWeights:
+    """One 4-bit weight matrix [n_out][k_in] for moe_linear, stored as one matrix of ExpertWeights: codes uint8
+    [N][K/2]; scales uint8 [N][K/32] (mxfp4), binary16 bits as uint8 pairs [N][K/16] (int4g32) or E4M3 [N][K/16]
+    (nvfp4); zeros uint8 [N][ceil(K/64)] (int4g32); tensor_scale fp32 [1] (nvfp4).  Rows may be strided."""
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "mxfp4",
+                 zeros: Optional[torch.Tensor] = None, tensor_scale: Optional[torch.Tensor] = None):
+        self.fmt, self.n_out, self.k_in = W_FORMATS[fmt], codes.shape[0], 2 * codes.shape[1]
+        K = self.k_in
+        p = moe_proj()
+
+        def rows(what, t, width):
+            if t is None or t.dtype != torch.uint8 or t.shape[0] != self.n_out or t.device != codes.device:
+                raise ValueError(f"LinearWeights: {what} must be uint8 [{self.n_out}][{width}] on {codes.device}")
+            return t.data_ptr(), _rows(f"LinearWeights: {what}", t, width)
+
+        p.w, p.w_row_stride = rows("codes", codes, K // 2)
+        p.scales, p.s_row_stride = rows("scales", scales, K // 32 if self.fmt == MOE_W_MXFP4 else K // 16)
+        if self.fmt == MOE_W_INT4_G32:
+            p.zeros, p.z_row_stride = rows("zeros", zeros, (K // 32 + 1) // 2)
+        elif self.fmt == MOE_W_NVFP4:
+            if tensor_scale is None or tensor_scale.device != codes.device:
+                raise ValueError(f"LinearWeights: nvfp4 needs a tensor_scale on {codes.device}")
+            _dense("LinearWeights: tensor_scale", tensor_scale, torch.float32, (1,))
+            p.tensor_scale = tensor_scale.data_ptr()
+        self.tensors = (codes, scales, zeros, tensor_scale)
+        self.device = codes.device
+        self.c = moe_linear_weights(self.fmt, self.n_out, K, p)
+        self.at = ctypes.addressof(self.c)
+
+
+def moe_linear_workspace_bytes(T: int, W: LinearWeights) -> int:
+    return lib().moe_linear_workspace_bytes(T, W.at)
+
+
+def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] = None,
+               dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None, workspace=None) -> torch.Tensor:
+    """x [T][k_in] bf16 (rows contiguous) times W^T, plus an fp32 bias [n_out] -> y [T][n_out] in `dtype` (or in
+    `out`'s type, whose rows may be strided)."""
+    T = x.shape[0]
+    dev = x.device
+    if W.device != dev or (bias is not None and bias.device != dev):
+        raise ValueError(f"moe_linear: x is on {dev}, the weights on {W.device}")
+    xs = _rows("moe_linear: x", x, W.k_in)
+    if bias is not None:
+        _dense("moe_linear: bias", bias, torch.float32, (W.n_out,))
+    if out is None:
+        out = torch.empty((T, W.n_out), dtype=dtype, device=dev)
+    elif out.shape[0] != T:
+        raise ValueError(f"moe_linear: {T} rows of x, {out.shape[0]} of out")
+    ys = _rows("moe_linear: out", out, W.n_out, dev)
+    ws = workspace if workspace is not None else _workspace(moe_linear_workspace_bytes(T, W), dev)
+    with _on(dev) as stream:
+        _check(lib().moe_linear(x.data_ptr(), _act_dtype(x), xs, T, W.at, None if bias is None else bias.data_ptr(),
+                                out.data_ptr(), _dtype("out", out), ys, None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel(), stream), "moe_linear")
+    return out
+
+
 # ----------------------------------------------------------------------------------------------------
 class MoELayer:
     """One routed-MoE layer with every intermediate buffer allocated once, so that forward() only
@@ -541,6 +825,71 @@ class MoELayer:
             moe_expert_ffn_mx(x, self.W, self.mx, self.buckets.offsets, self.buckets.sorted_slot, self.k_total,
                               out=self.y_slots, workspace=self.ffn_ws)
         return moe_combine(self.y_slots, self.weights, out=self.y)
+
+
+class MoEBlock:
+    """The MoE half of a decoder block, every buffer allocated once for T tokens so that forward() only enqueues
+    library calls (capturable in a HIP graph): the attention output's projection (4-bit weights; left out
+    without W_o), the residual addition and norm, routing by a rule, bucketing, the expert FFN and the combine.
+    With mx ("fp8", "fp6", "fp4") the norm writes the MX codes that the expert FFN reads.
+
+    forward(attn, residual) -> (y fp32 [T][H], residual_out): the next block's norm adds y to residual_out."""
+
+    def __init__(self, W: ExpertWeights, T: int, rule: RouteRule, w_router: torch.Tensor, norm: RmsNorm,
+                 W_o: Optional[LinearWeights] = None, mx=None):
+        self.W, self.T, self.rule, self.w_router, self.norm, self.W_o = W, T, rule, w_router, norm, W_o
+        self.mx = None if mx is None else _mx_fmt(mx)
+        dev, H = W.device, W.hidden
+        E = W.n_experts - rule.n_shared
+        if w_router.shape != (E, H) or norm.hidden != H or (W_o is not None and W_o.n_out != H):
+            raise ValueError(f"MoEBlock: hidden {H} and {E} routed experts do not fit the router, norm or projection")
+        kt = self.k_total = rule.top_k + rule.n_shared
+        n = T * kt
+        act = torch.float16 if W.fmt == MOE_W_FP16 else torch.bfloat16
+        self.a = None if W_o is None else torch.empty((T, H), dtype=torch.float32, device=dev)
+        self.linear_ws = None if W_o is None else _workspace(moe_linear_workspace_bytes(T, W_o), dev)
+        self.x = torch.empty((T, H), dtype=act, device=dev)
+        self.codes = self.scales = None
+        if self.mx is not None:
+            self.codes = torch.empty((T, moe_mx_row_bytes(self.mx, H)), dtype=torch.uint8, device=dev)
+            self.scales = torch.empty((T, H // 32), dtype=torch.uint8, device=dev)
+        self.ids = torch.empty((T, kt), dtype=torch.int32, device=dev)
+        self.weights = torch.empty((T, kt), dtype=torch.float32, device=dev)
+        self.route_ws = _workspace(moe_route_workspace_bytes(T, H, E), dev)
+        self.buckets = Buckets(torch.empty(W.n_experts, dtype=torch.int32, device=dev),
+                               torch.empty(W.n_experts + 1, dtype=torch.int32, device=dev),
+                               torch.empty(n, dtype=torch.int32, device=dev),
+                               torch.empty(n, dtype=torch.int32, device=dev))
+        self.bucket_ws = _workspace(moe_bucket_workspace_bytes(n, W.n_experts), dev)
+        # A bias of -inf may leave slots empty (id -1, weight 0).  The FFN does not write their rows, and 0 times
+        # what an earlier pass left there could be NaN: such a rule clears the rows in every pass.
+        self.clear = rule.selection_bias is not None and not bool(torch.isfinite(rule.selection_bias).all())
+        self.y_slots = torch.zeros((n, H), dtype=torch.float32, device=dev)
+        self.ffn_ws = _workspace(moe_expert_ffn_workspace_bytes(T, kt, W) if self.mx is None
+                                 else moe_expert_ffn_mx_workspace_bytes(T, kt, W, self.mx), dev)
+        self.y = torch.empty((T, H), dtype=torch.float32, device=dev)
+
+    def forward(self, attn: torch.Tensor, residual: torch.Tensor, residual_out: Optional[torch.Tensor] = None):
+        if attn.shape[0] != self.T:
+            raise ValueError(f"MoEBlock: {attn.shape[0]} rows, built for {self.T}")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        a = attn
+        if self.W_o is not None:
+            a = moe_linear(attn, self.W_o, out=self.a, workspace=self.linear_ws)
+        moe_add_rms_norm(a, self.norm, residual, mx=self.mx, out=(self.x, residual_out, self.codes, self.scales))
+        moe_route_grouped(self.x, self.w_router, self.rule, out=(self.ids, self.weights, None),
+                          workspace=self.route_ws)
+        b = moe_bucket(self.ids, self.W.n_experts, out=self.buckets, workspace=self.bucket_ws)
+        if self.clear:
+            self.y_slots.zero_()
+        if self.mx is None:
+            moe_expert_ffn(self.x, self.W, b.offsets, b.sorted_slot, self.k_total, out=self.y_slots,
+                           workspace=self.ffn_ws)
+        else:
+            moe_expert_ffn_mx_codes(self.codes, self.scales, self.W, self.mx, b.offsets, b.sorted_slot, self.k_total,
+                                    out=self.y_slots, workspace=self.ffn_ws)
+        return moe_combine(self.y_slots, self.weights, out=self.y), residual_out
 
 
 class FixedShapeLayer:
@@ -628,4 +977,5 @@ __all__ = ["moe_route", "moe_route_sigmoid", "moe_route_bucket", "moe_route_buck
            "moe_expert_ffn_mx", "moe_expert_ffn_mx_workspace_bytes", "moe_stream_read", "moe_expert_ffn_mx_workspace_layout",
            "moe_route_workspace_bytes", "moe_bucket_workspace_bytes", "moe_expert_ffn_workspace_bytes",
            "moe_row_shape", "moe_pad_rows", "ExpertWeights", "Buckets", "MoELayer", "FixedShapeLayer", "MoEError",
-           "lib"]
+           "moe_select_experts", "moe_route_grouped", "moe_add_rms_norm", "moe_linear", "moe_linear_workspace_bytes",
+           "moe_expert_ffn_mx_codes", "RouteRule", "RmsNorm", "LinearWeights", "MoEBlock", "lib"]

@@ -478,16 +478,18 @@ moe_status moe_expert_ffn_mx_workspace_layout(int T, int k_total, const moe_expe
   return MOE_OK;
 }
 
-moe_status moe_expert_ffn_mx(const void* x, moe_act_dtype x_dtype, int T, int k_total, const moe_expert_weights* W,
-                             moe_mx_format fmt, const int32_t* offsets, const int32_t* sorted_slot, float* y_slots,
-                             void* workspace, size_t workspace_bytes, void* stream) {
-  if (T == 0) return MOE_OK;
-  if (!W) return MOE_ERR_NULL;
-  if (T < 0 || k_total < 1 || k_total > MOE_MAX_SLOTS_PER_TOKEN) return MOE_ERR_SHAPE;
-  if (W->fmt != MOE_W_MXFP4 || x_dtype != MOE_ACT_BF16 || moe::mx_bits(fmt) == 0) return MOE_ERR_DTYPE;
+}  // extern "C"
+
+namespace {
+
+// moe_expert_ffn_mx (x non-NULL where need_x) and moe_expert_ffn_mx_codes (x_codes and x_scales).
+moe_status run_ffn_mx(bool from_codes, const void* x, const uint8_t* x_codes, const uint8_t* x_scales, int T,
+                      int k_total, const moe_expert_weights* W, moe_mx_format fmt, const int32_t* offsets,
+                      const int32_t* sorted_slot, float* y_slots, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   if (W->n_experts < 1 || W->n_experts > MOE_MAX_EXPERTS || W->hidden < 1 || W->inter < 1) return MOE_ERR_SHAPE;
   if ((int64_t)T * k_total > INT_MAX) return MOE_ERR_SHAPE;
-  if (!x || !offsets || !sorted_slot || !y_slots) return MOE_ERR_NULL;
+  if ((from_codes ? !x_codes || !x_scales : !x) || !offsets || !sorted_slot || !y_slots) return MOE_ERR_NULL;
   const int H = W->hidden, I = W->inter;
   moe_status st;
   if ((st = check_proj(W->gate, W->fmt, W->n_experts, I, H)) != MOE_OK) return st;
@@ -503,7 +505,9 @@ moe_status moe_expert_ffn_mx(const void* x, moe_act_dtype x_dtype, int T, int k_
   if ((int64_t)T * (int64_t)moe_mx_row_bytes(fmt, H) >= INT32_MAX ||
       n_slots * (int64_t)moe_mx_row_bytes(fmt, I) >= INT32_MAX)
     return MOE_ERR_SHAPE;
-  if (!al16(x) || !al16(y_slots) || !al4(offsets) || !al4(sorted_slot)) return MOE_ERR_ALIGN;
+  if ((from_codes ? !al16(x_codes) || !al4(x_scales) : !al16(x)) || !al16(y_slots) || !al4(offsets) ||
+      !al4(sorted_slot))
+    return MOE_ERR_ALIGN;
   const MxWs w = mx_ws(T, k_total, W, fmt);
   if (!workspace || workspace_bytes < w.total) return MOE_ERR_WORKSPACE;
   if (!al16(workspace)) return MOE_ERR_ALIGN;
@@ -522,12 +526,40 @@ moe_status moe_expert_ffn_mx(const void* x, moe_act_dtype x_dtype, int T, int k_
   a.offsets = offsets;
   a.sorted_slot = sorted_slot;
   a.y_slots = y_slots;
-  a.xq = ws + w.xq;
-  a.xs = ws + w.xs;
+  a.xq = from_codes ? const_cast<uint8_t*>(x_codes) : ws + w.xq;  // (read only by launch_ffn_mx_codes)
+  a.xs = from_codes ? const_cast<uint8_t*>(x_scales) : ws + w.xs;
   a.hq = ws + w.hq;
   a.hs = ws + w.hs;
   a.table = ws + w.table;
-  return hip_status(moe::launch_ffn_mx(a, (hipStream_t)stream));
+  return hip_status(from_codes ? moe::launch_ffn_mx_codes(a, (hipStream_t)stream)
+                               : moe::launch_ffn_mx(a, (hipStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_expert_ffn_mx(const void* x, moe_act_dtype x_dtype, int T, int k_total, const moe_expert_weights* W,
+                             moe_mx_format fmt, const int32_t* offsets, const int32_t* sorted_slot, float* y_slots,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (T == 0) return MOE_OK;
+  if (!W) return MOE_ERR_NULL;
+  if (T < 0 || k_total < 1 || k_total > MOE_MAX_SLOTS_PER_TOKEN) return MOE_ERR_SHAPE;
+  if (W->fmt != MOE_W_MXFP4 || x_dtype != MOE_ACT_BF16 || moe::mx_bits(fmt) == 0) return MOE_ERR_DTYPE;
+  return run_ffn_mx(false, x, nullptr, nullptr, T, k_total, W, fmt, offsets, sorted_slot, y_slots, workspace,
+                    workspace_bytes, stream);
+}
+
+moe_status moe_expert_ffn_mx_codes(const uint8_t* x_codes, const uint8_t* x_scales, int T, int k_total,
+                                   const moe_expert_weights* W, moe_mx_format fmt, const int32_t* offsets,
+                                   const int32_t* sorted_slot, float* y_slots, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  if (T == 0) return MOE_OK;
+  if (!W) return MOE_ERR_NULL;
+  if (T < 0 || k_total < 1 || k_total > MOE_MAX_SLOTS_PER_TOKEN) return MOE_ERR_SHAPE;
+  if (W->fmt != MOE_W_MXFP4 || moe::mx_bits(fmt) == 0) return MOE_ERR_DTYPE;
+  return run_ffn_mx(true, nullptr, x_codes, x_scales, T, k_total, W, fmt, offsets, sorted_slot, y_slots, workspace,
+                    workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -627,6 +659,155 @@ moe_status moe_route_bucket(const void* x, moe_act_dtype x_dtype, int T, int H, 
   if (err != hipSuccess) return MOE_ERR_HIP;
   if (moe::bucket_plans_inline(T * k_total)) return MOE_OK;
   return hip_status(moe::launch_ffn_plan(T, k_total, W->n_experts, plan_opts(W, T, k_total), offsets, table, st));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// What stands in front of the layer: residual addition and norm, routing by a rule, 4-bit products.
+namespace {
+
+inline int dt_bytes(int dt) { return dt == MOE_DT_FP32 ? 4 : 2; }
+inline bool known_dt(int dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_FP16 || dt == MOE_DT_FP32; }
+inline bool al_value(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(dt_bytes(dt) - 1)) == 0; }
+inline bool finite(float v) { return v - v == 0.0f; }
+
+moe_status check_rule(const moe_route_rule* r, int T, int E) {
+  if (!r) return MOE_ERR_NULL;
+  if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || r->n_shared < 0) return MOE_ERR_SHAPE;
+  if ((r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) ||
+      (r->group_score != MOE_GROUP_TOP2 && r->group_score != MOE_GROUP_MAX))
+    return MOE_ERR_DTYPE;
+  if (r->n_groups < 1 || r->n_groups > MOE_MAX_GROUPS || E % r->n_groups != 0 || r->topk_groups < 1 ||
+      r->topk_groups > r->n_groups)
+    return MOE_ERR_SHAPE;
+  if (!finite(r->routed_scale) || !finite(r->shared_weight)) return MOE_ERR_SHAPE;
+  if (r->top_k < 1 || r->top_k > r->topk_groups * (E / r->n_groups) ||
+      (int64_t)r->top_k + r->n_shared > MOE_MAX_SLOTS_PER_TOKEN)
+    return MOE_ERR_TOPK;
+  if ((int64_t)T * (r->top_k + r->n_shared) > INT_MAX || (int64_t)T * E > INT_MAX) return MOE_ERR_SHAPE;
+  if (r->selection_bias && !al4(r->selection_bias)) return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_select_experts(const void* logits, moe_dtype logits_dtype, int64_t row_stride, int T, int E,
+                              const moe_route_rule* rule, int32_t* ids, float* weights, float* scores,
+                              void* stream) {
+  if (T == 0) return MOE_OK;
+  const moe_status st = check_rule(rule, T, E);
+  if (st != MOE_OK) return st;
+  if (!known_dt(logits_dtype)) return MOE_ERR_DTYPE;
+  if (!logits || !ids || !weights) return MOE_ERR_NULL;
+  if (row_stride < E || row_stride > INT64_MAX / 4 / T) return MOE_ERR_SHAPE;
+  if (!al_value(logits, logits_dtype) || !al4(ids) || !al4(weights) || (scores && !al4(scores))) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_select(logits, logits_dtype, row_stride, T, E, *rule, ids, weights, scores,
+                                       (hipStream_t)stream));
+}
+
+moe_status moe_route_grouped(const void* x, moe_act_dtype x_dtype, int T, int H, const float* w_router, int E,
+                             const moe_route_rule* rule, int32_t* ids, float* weights, float* scores,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (T == 0) return MOE_OK;
+  const moe_status st = check_rule(rule, T, E);
+  if (st != MOE_OK) return st;
+  if (H < 1) return MOE_ERR_SHAPE;
+  if (x_dtype != MOE_ACT_BF16 && x_dtype != MOE_ACT_FP16) return MOE_ERR_DTYPE;
+  if (!x || !w_router || !ids || !weights) return MOE_ERR_NULL;
+  if (!al16(x) || !al4(w_router) || !al4(ids) || !al4(weights) || (scores && !al4(scores))) return MOE_ERR_ALIGN;
+  const size_t need = moe_route_workspace_bytes(T, H, E);
+  if (!workspace || workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (!al16(workspace)) return MOE_ERR_ALIGN;
+  return hip_status(moe::launch_route_grouped(x, x_dtype == MOE_ACT_FP16, T, H, w_router, E, *rule, ids, weights,
+                                              scores, (float*)workspace, (hipStream_t)stream));
+}
+
+moe_status moe_add_rms_norm(const moe_norm* norm, const void* x, moe_dtype x_dtype, int64_t x_row_stride,
+                            const void* residual, moe_dtype residual_dtype, int64_t residual_row_stride, int T,
+                            void* residual_out, int64_t residual_out_row_stride, void* y, moe_dtype y_dtype, int fmt,
+                            uint8_t* codes, uint8_t* scales, void* stream) {
+  if (T == 0) return MOE_OK;
+  if (!norm) return MOE_ERR_NULL;
+  const int H = norm->hidden;
+  if (T < 0 || H < 1 || !(norm->eps >= 0.0f) || !finite(norm->eps)) return MOE_ERR_SHAPE;
+  if (!known_dt(x_dtype) || !known_dt(norm->weight_dtype) || (residual && !known_dt(residual_dtype)) ||
+      (y && !known_dt(y_dtype)) || (fmt != 0 && moe::mx_bits(fmt) == 0))
+    return MOE_ERR_DTYPE;
+  if (!x || !norm->weight || (residual_out && !residual) || (!y && fmt == 0)) return MOE_ERR_NULL;
+  if (fmt != 0 ? !codes || !scales : codes || scales) return MOE_ERR_NULL;
+  if (fmt != 0 && H % 32 != 0) return MOE_ERR_BLOCK;
+  const int64_t most = INT64_MAX / 4 / T;
+  if (x_row_stride < H || x_row_stride > most || (residual && (residual_row_stride < H || residual_row_stride > most)) ||
+      (residual_out && (residual_out_row_stride < H || residual_out_row_stride > most)))
+    return MOE_ERR_SHAPE;
+  if (!al_value(x, x_dtype) || !al_value(norm->weight, norm->weight_dtype) ||
+      (residual && !al_value(residual, residual_dtype)) || (residual_out && !al_value(residual_out, residual_dtype)) ||
+      (y && !al_value(y, y_dtype)) || (fmt != 0 && !al16(codes)))
+    return MOE_ERR_ALIGN;
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = norm->weight;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.codes = codes;
+  a.scales = scales;
+  a.x_stride = x_row_stride;
+  a.r_stride = residual_row_stride;
+  a.ro_stride = residual_out_row_stride;
+  a.code_row = fmt != 0 ? (int64_t)moe_mx_row_bytes((moe_mx_format)fmt, H) : 0;
+  a.x_dt = x_dtype;
+  a.r_dt = residual_dtype;
+  a.w_dt = norm->weight_dtype;
+  a.y_dt = y_dtype;
+  a.T = T;
+  a.H = H;
+  a.mx = fmt;
+  a.eps = norm->eps;
+  return hip_status(moe::launch_norm(a, (hipStream_t)stream));
+}
+
+size_t moe_linear_workspace_bytes(int T, const moe_linear_weights* W) {
+  if (!W || T <= 0 || W->n_out <= 0 || W->k_in <= 0) return 0;
+  return round_up(moe::linear_workspace_bytes(T, W->fmt, W->n_out, W->k_in), 256);
+}
+
+moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride, int T, const moe_linear_weights* W,
+                      const float* bias, void* y, moe_dtype y_dtype, int64_t y_row_stride, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (T == 0) return MOE_OK;
+  if (!W) return MOE_ERR_NULL;
+  if (T < 0 || W->n_out < 1 || W->k_in < 1) return MOE_ERR_SHAPE;
+  if (!known_format(W->fmt) || W->fmt == MOE_W_FP16 || x_dtype != MOE_ACT_BF16 || !known_dt(y_dtype))
+    return MOE_ERR_DTYPE;
+  if (!x || !y) return MOE_ERR_NULL;
+  const moe_status st = check_proj(W->w, W->fmt, 1, W->n_out, W->k_in);
+  if (st != MOE_OK) return st;
+  const int64_t most = INT64_MAX / 4 / T;
+  if (W->w.w_row_stride >= (int64_t)1 << 25 || x_row_stride < W->k_in || x_row_stride > most ||
+      y_row_stride < W->n_out || y_row_stride > most)
+    return MOE_ERR_SHAPE;
+  if (!al16(x) || x_row_stride % 8 != 0 || !al_value(y, y_dtype) || (bias && !al4(bias))) return MOE_ERR_ALIGN;
+  const size_t need = moe_linear_workspace_bytes(T, W);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!al16(workspace)) return MOE_ERR_ALIGN;
+  moe::LinArgs a{};
+  a.x = (const uint16_t*)x;
+  a.x_stride = x_row_stride;
+  a.T = T;
+  a.N = W->n_out;
+  a.K = W->k_in;
+  a.fmt = W->fmt;
+  a.w = dev(W->w);
+  a.bias = bias;
+  a.y = y;
+  a.y_dt = y_dtype;
+  a.y_stride = y_row_stride;
+  a.ws = workspace;
+  return hip_status(moe::launch_linear(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

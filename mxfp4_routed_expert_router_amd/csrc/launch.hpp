@@ -18,6 +18,17 @@ hipError_t launch_route(const void* x, int x_fp16, int T, int H, const float* w_
                         float* partial, int splits, hipStream_t stream, bool sigmoid = false,
                         float routed_scale = 1.0f, float shared_weight = 1.0f);
 
+// The router's logits alone: partial sums [splits][T][E].
+hipError_t launch_route_logits(const void* x, int x_fp16, int T, int H, const float* w_router, int E, float* partial,
+                               int splits, hipStream_t stream);
+
+// ---- choice of experts by a rule (scores, bias, groups, top-k), from logits or from x ----
+hipError_t launch_select(const void* logits, int dt, int64_t row_stride, int T, int E, const moe_route_rule& rule,
+                         int32_t* ids, float* weights, float* scores, hipStream_t stream);
+hipError_t launch_route_grouped(const void* x, int x_fp16, int T, int H, const float* w_router, int E,
+                                const moe_route_rule& rule, int32_t* ids, float* weights, float* scores,
+                                float* partial, hipStream_t stream);
+
 // Router, bucketing and (table != NULL) the expert FFN's tile table in two launches (logits, then
 // one workgroup that selects, buckets and plans), for the small calls route_bucket_fusable()
 // accepts (at most 8 tokens).
@@ -122,6 +133,37 @@ hipError_t launch_mx_quantize(const void* x, bool x_fp16, int64_t n_rows, int K,
                               uint8_t* scales, hipStream_t stream);
 // x quantisation, tile table, gate/up (writes h codes), down (writes y_slots).
 hipError_t launch_ffn_mx(const MxFfnArgs& a, hipStream_t stream);
+
+// launch_ffn_mx on x codes and scales that the caller has (a.xq, a.xs are read, a.x is not used).
+hipError_t launch_ffn_mx_codes(const MxFfnArgs& a, hipStream_t stream);
+
+// ---- residual addition + RMS norm ----
+struct NormArgs {
+  const void *x, *residual;  // [T] rows at x_stride / r_stride values; residual may be NULL
+  const void* weight;        // [H]
+  void *residual_out, *y;    // either may be NULL; y rows are H values apart
+  uint8_t *codes, *scales;   // mx != 0
+  int64_t x_stride, r_stride, ro_stride, code_row;  // code_row: bytes of a packed row
+  int x_dt, r_dt, w_dt, y_dt;                       // moe_dtype
+  int T, H, mx;                                     // mx: moe_mx_format, 0 for none
+  float eps;
+};
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
+
+// ---- products with 4-bit weights ----
+struct LinArgs {
+  const uint16_t* x;  // [T] rows of K bf16 values, x_stride values apart
+  int64_t x_stride;
+  int T, N, K, fmt;
+  ProjDev w;          // expert strides unused; ts: one value
+  const float* bias;  // [N] or NULL
+  void* y;
+  int y_dt;
+  int64_t y_stride;
+  void* ws;
+};
+size_t linear_workspace_bytes(int T, int fmt, int N, int K);
+hipError_t launch_linear(const LinArgs& a, hipStream_t stream);
 
 // ---- combine ----
 hipError_t launch_combine(const float* y_slots, const float* weights, int T, int k_total, int H, float* y,

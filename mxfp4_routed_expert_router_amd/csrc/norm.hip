@@ -1,0 +1,199 @@
+// Residual addition and root-mean-square norm, with an optional MX output (8-, 6- or 4-bit codes with one E8M0
+// scale per 32 values, the layout the MX expert FFN reads).  Per row of H values:
+//   s = x + residual                      (fp32; residual_out = s rounded to the residual's type)
+//   r = 1 / sqrt(sum(s^2) / H + eps)      (fp32 sum: per-thread partial sums, then a fixed tree)
+//   y = s * r * weight                    (fp32; rounded once to y's type)
+//   codes, scales = MX blocks of the fp32 y (not of the rounded one: one rounding, not two)
+// It reads x and residual and writes residual_out, y and the codes once each, so the bytes bound it; the row
+// stays in registers between the sum and the outputs.
+#include "launch.hpp"
+#include "mx.hpp"
+#include "values.hpp"
+
+namespace moe {
+
+namespace {
+
+// Sum of v over the workgroup, the same value in every thread (fixed order: waves in wave order).
+// red: one float per wave.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  const int wave = threadIdx.x >> 6, n = (blockDim.x + 63) >> 6;
+  v = wave_sum_dpp(v);
+  if (n == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[wave] = v;
+  __syncthreads();
+  float s = 0.0f;
+  for (int w = 0; w < n; ++w) s += red[w];
+  return s;
+}
+
+// Codes and scale of a 32-value block held by four consecutive lanes, eight values each (element i of the
+// row is the first of this lane's).
+template <int F>
+__device__ __forceinline__ void store_quarter(const float (&y)[8], uint8_t* __restrict__ codes_row,
+                                              uint8_t* __restrict__ scales_row, int i, bool ok) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));
+  amax = fmaxf(amax, __shfl_xor(amax, 1, kWave));
+  amax = fmaxf(amax, __shfl_xor(amax, 2, kWave));
+  const uint32_t sc = mx_scale_code<F>(amax);
+  uint32_t dw[2];
+  mx_pack_quarter<F>(y, mx_inv_scale(sc), dw);
+  const int q = (i >> 3) & 3;
+  uint8_t* blk = codes_row + (int64_t)(i >> 5) * (4 * Mx<F>::kBits);
+  if constexpr (Mx<F>::kBits == 6) {  // 6 bytes per lane: pairs of lanes write 12
+    const uint32_t o0 = (uint32_t)__shfl_xor((int)dw[0], 1, kWave);
+    const uint32_t o1 = (uint32_t)__shfl_xor((int)dw[1], 1, kWave);
+    if (ok && (q & 1) == 0) {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(blk + 6 * q);
+      dst[0] = dw[0];
+      dst[1] = (dw[1] & 0xFFFFu) | (o0 << 16);
+      dst[2] = (o0 >> 16) | (o1 << 16);
+    }
+  } else if constexpr (Mx<F>::kBits == 8) {
+    if (ok) *reinterpret_cast<u32x2*>(blk + 8 * q) = u32x2{dw[0], dw[1]};
+  } else {
+    if (ok) *reinterpret_cast<uint32_t*>(blk + 4 * q) = dw[0];
+  }
+  if (ok && q == 0) scales_row[i >> 5] = (uint8_t)sc;
+}
+
+// One row per workgroup; a thread holds NV runs of eight consecutive values (run v at 8 (v * threads + tid)).
+// RD: the residual's type, or -1 without one.
+template <int XD, int RD, int NV>
+__global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
+  __shared__ float red[16];
+  const int64_t t = blockIdx.x;
+  const int H = a.H;
+  constexpr int RT = RD < 0 ? MOE_DT_BF16 : RD;
+  Raw8<XD> xr[NV];
+  Raw8<RT> rr[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {  // runs past the row read its first run and are not used
+    const int i = 8 * (v * (int)blockDim.x + (int)threadIdx.x), c = i < H ? i : 0;
+    xr[v] = ld_raw8<XD>(a.x, t * a.x_stride + c);
+    if constexpr (RD >= 0) rr[v] = ld_raw8<RT>(a.residual, t * a.r_stride + c);
+  }
+  float s[NV][8], sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = 8 * (v * (int)blockDim.x + (int)threadIdx.x);
+    raw8_to_f32(xr[v], s[v]);
+    if constexpr (RD >= 0) {
+      float r[8];
+      raw8_to_f32(rr[v], r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[v][j] += r[j];
+      if (a.residual_out && i < H) st8_as<RT>(a.residual_out, t * a.ro_stride + i, s[v]);
+    }
+    float p = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p = __builtin_fmaf(s[v][j], s[v][j], p);
+    sum += i < H ? p : 0.0f;
+  }
+  const float rstd = 1.0f / sqrtf(block_sum(sum, red) / (float)H + a.eps);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int i = 8 * (v * (int)blockDim.x + (int)threadIdx.x);
+    const bool ok = i < H;
+    float w[8], y[8];
+    ld8(a.weight, a.w_dt, ok ? i : 0, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = s[v][j] * rstd * w[j];
+    if (a.y && ok) st8(a.y, a.y_dt, t * H + i, y);
+    if (a.mx) {  // the four lanes of a block are all inside the row or all outside (H % 32 == 0)
+      uint8_t* cr = a.codes + t * a.code_row;
+      uint8_t* sr = a.scales + t * (H >> 5);
+      if (a.mx == MOE_MX_FP8_E4M3) store_quarter<MOE_MX_FP8_E4M3>(y, cr, sr, i, ok);
+      else if (a.mx == MOE_MX_FP6_E2M3) store_quarter<MOE_MX_FP6_E2M3>(y, cr, sr, i, ok);
+      else store_quarter<MOE_MX_FP4_E2M1>(y, cr, sr, i, ok);
+    }
+  }
+}
+
+// Any length, alignment and stride: two passes over the row, one value at a time (the second pass finds it in
+// the caches).  residual_out may be residual itself, so the second pass reads a value before it writes it.
+template <int F>
+__device__ __forceinline__ void norm_block(const NormArgs& a, int64_t t, int b, float rstd) {
+  float y[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const int i = 32 * b + j;
+    float s = ld_value(a.x, a.x_dt, t * a.x_stride + i);
+    if (a.residual) s += ld_value(a.residual, a.r_dt, t * a.r_stride + i);
+    y[j] = s * rstd * ld_value(a.weight, a.w_dt, i);
+  }
+  uint32_t dw[8];
+  const uint32_t sc = mx_pack_block<F>(y, dw);
+  mx_store_block<F>(a.codes + t * a.code_row + (int64_t)b * (4 * Mx<F>::kBits), dw);
+  a.scales[t * (a.H >> 5) + b] = (uint8_t)sc;
+}
+
+__global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a) {
+  __shared__ float red[16];
+  const int64_t t = blockIdx.x;
+  const int H = a.H;
+  float sum = 0.0f;
+  for (int i = threadIdx.x; i < H; i += 256) {
+    float s = ld_value(a.x, a.x_dt, t * a.x_stride + i);
+    if (a.residual) s += ld_value(a.residual, a.r_dt, t * a.r_stride + i);
+    sum = __builtin_fmaf(s, s, sum);
+  }
+  const float rstd = 1.0f / sqrtf(block_sum(sum, red) / (float)H + a.eps);
+  if (a.mx) {  // before residual_out is written: it may be residual
+    for (int b = threadIdx.x; b < (H >> 5); b += 256) {
+      if (a.mx == MOE_MX_FP8_E4M3) norm_block<MOE_MX_FP8_E4M3>(a, t, b, rstd);
+      else if (a.mx == MOE_MX_FP6_E2M3) norm_block<MOE_MX_FP6_E2M3>(a, t, b, rstd);
+      else norm_block<MOE_MX_FP4_E2M1>(a, t, b, rstd);
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < H; i += 256) {
+    float s = ld_value(a.x, a.x_dt, t * a.x_stride + i);
+    if (a.residual) s += ld_value(a.residual, a.r_dt, t * a.r_stride + i);
+    if (a.residual_out) st_value(a.residual_out, a.r_dt, t * a.ro_stride + i, s);
+    if (a.y) st_value(a.y, a.y_dt, t * H + i, s * rstd * ld_value(a.weight, a.w_dt, i));
+  }
+}
+
+template <int XD, int RD>
+void launch_norm_vec(const NormArgs& a, int threads, int nv, hipStream_t stream) {
+  const dim3 g((unsigned)a.T);
+  if (nv == 1) norm_kernel<XD, RD, 1><<<g, threads, 0, stream>>>(a);
+  else if (nv == 2) norm_kernel<XD, RD, 2><<<g, threads, 0, stream>>>(a);
+  else norm_kernel<XD, RD, 4><<<g, threads, 0, stream>>>(a);
+}
+template <int XD>
+void launch_norm_x(const NormArgs& a, int threads, int nv, hipStream_t stream) {
+  if (!a.residual) launch_norm_vec<XD, -1>(a, threads, nv, stream);
+  else if (a.r_dt == MOE_DT_BF16) launch_norm_vec<XD, MOE_DT_BF16>(a, threads, nv, stream);
+  else if (a.r_dt == MOE_DT_FP16) launch_norm_vec<XD, MOE_DT_FP16>(a, threads, nv, stream);
+  else launch_norm_vec<XD, MOE_DT_FP32>(a, threads, nv, stream);
+}
+
+inline bool runs_of_16(const void* p, int64_t stride, int dt) {
+  return ((uintptr_t)p & 15u) == 0 && stride % (dt == MOE_DT_FP32 ? 4 : 8) == 0;
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  const bool vec = a.H % 8 == 0 && a.H <= 8 * 1024 * 4 && runs_of_16(a.x, a.x_stride, a.x_dt) &&
+                   (!a.residual || runs_of_16(a.residual, a.r_stride, a.r_dt)) &&
+                   (!a.residual_out || runs_of_16(a.residual_out, a.ro_stride, a.r_dt)) &&
+                   runs_of_16(a.weight, 0, a.w_dt) && (!a.y || runs_of_16(a.y, 0, a.y_dt));
+  if (!vec) {
+    norm_any_kernel<<<dim3((unsigned)a.T), 256, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  const int runs = a.H / 8;
+  const int nv = runs <= 1024 ? 1 : (runs <= 2048 ? 2 : 4);
+  const int threads = ((runs + nv - 1) / nv + 63) / 64 * 64;
+  if (a.x_dt == MOE_DT_BF16) launch_norm_x<MOE_DT_BF16>(a, threads, nv, stream);
+  else if (a.x_dt == MOE_DT_FP16) launch_norm_x<MOE_DT_FP16>(a, threads, nv, stream);
+  else launch_norm_x<MOE_DT_FP32>(a, threads, nv, stream);
+  return hipGetLastError();
+}
+
+}  // namespace moe
