@@ -4,7 +4,10 @@
 // Weights are decoded in registers into bf16 MFMA operands whose values are exact: E2M1 times a power of two
 // (MXFP4) or times an E4M3 scale (NVFP4, at most 6 significant bits) in one operand, (code - zero) * scale
 // (INT4, at most 15 bits) as a high and a low operand.  Products are exact in fp32; the fp32 sums round.
+#include <algorithm>
+
 #include "launch.hpp"
+#include "tiles.hpp"
 #include "values.hpp"
 
 namespace moe {
@@ -18,32 +21,7 @@ struct Blk {
   float s0, s1;  // MXFP4: s0; NVFP4: the two 16-value scales; INT4: scale and -zero * scale
 };
 
-__device__ __forceinline__ float e4m3_value(uint32_t c) {  // bias 7, subnormals at exponent field 0
-  const uint32_t ex = (c >> 3) & 15u, fr = c & 7u;
-  const float mag = ex ? __uint_as_float(((ex + 120u) << 23) | (fr << 20)) : (float)fr * 0.001953125f;
-  return (c & 0x80u) ? -mag : mag;
-}
-
-template <int FMT>
-__device__ __forceinline__ Blk<FMT> load_block(const LinArgs& a, int n, int b, bool ok) {
-  Blk<FMT> r;
-  r.q = u32x4{0, 0, 0, 0};
-  r.s0 = r.s1 = 0.0f;
-  if (!ok) return r;  // a scale of zero: zero weights
-  r.q = ld16(a.w.w + (int64_t)n * a.w.wr + 16 * (int64_t)b);
-  const uint8_t* s = a.w.s + (int64_t)n * a.w.sr;
-  if constexpr (FMT == MOE_W_MXFP4) {
-    r.s0 = e8m0_to_f32(s[b]);
-  } else if constexpr (FMT == MOE_W_INT4_G32) {
-    r.s0 = (float)bitcast<_Float16>((uint16_t)(s[2 * b] | (s[2 * b + 1] << 8)));
-    const uint32_t z = (a.w.z[(int64_t)n * a.w.zr + (b >> 1)] >> (4 * (b & 1))) & 15u;
-    r.s1 = -(float)z * r.s0;
-  } else {
-    r.s0 = e4m3_value(s[2 * b]);
-    r.s1 = e4m3_value(s[2 * b + 1]);
-  }
-  return r;
-}
+__device__ __forceinline__ float e4m3_value(uint32_t c) { return __builtin_amdgcn_cvt_f32_fp8((int)c, 0); }
 
 __device__ __forceinline__ uint32_t pack_high(float a, float b) {  // the upper halves of two floats
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
@@ -77,80 +55,681 @@ __device__ __forceinline__ bf16x8 decode(const Blk<FMT>& r, int s, bf16x8& lo) {
   }
 }
 
-// 16 rows of W times 16 MT tokens per workgroup; its four waves take every fourth step of 128 values of K and
-// their sums meet in LDS.  Lane (r = lane % 16, q = lane / 16) holds row r's block 4 step + q.
-template <int FMT, int MT>
-__global__ __launch_bounds__(256) void linear_rows_kernel(LinArgs a) {
-  __shared__ float part[4][MT][16][17];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, l16 = lane & 15, q = lane >> 4;
-  const int n = blockIdx.x * 16 + l16, t0 = blockIdx.y * 16 * MT;
-  const int blocks = a.K / 32;
-  f32x4 acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = 4 * wave; b0 < blocks; b0 += 16) {
-    const int b = b0 + q;
-    const Blk<FMT> w = load_block<FMT>(a, n, b, n < a.N && b < blocks);
-    bf16x8 x[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int t = t0 + 16 * m + l16;
-      const bool ok = t < a.T && b < blocks;
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        x[m][s] = bitcast<bf16x8>(ok ? ld16(a.x + (int64_t)t * a.x_stride + 32 * (int64_t)b + 8 * s) : u32x4{0, 0, 0, 0});
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      bf16x8 lo;
-      const bf16x8 hi = decode<FMT>(w, s, lo);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, x[m][s], acc[m], 0, 0, 0);
-        if constexpr (FMT == MOE_W_INT4_G32)
-          acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, x[m][s], acc[m], 0, 0, 0);
-      }
+// Bytes at any address through a buffer descriptor (u8 or u16; offsets need no alignment).
+template <int FMT>
+__device__ __forceinline__ uint32_t bld_scale(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff) {
+  if constexpr (FMT == MOE_W_MXFP4) return __builtin_amdgcn_raw_buffer_load_b8(r, off, soff, 0);
+  return __builtin_amdgcn_raw_buffer_load_b16(r, off, soff, 0);
+}
+// A block's scale data in one word: the scale bytes, and for INT4 its zero point in bits 16 .. 19 (odd: the block's
+// index is odd, its zero point is the high nibble of the byte z).
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_word(uint32_t s, uint32_t z, int odd) {
+  return FMT == MOE_W_INT4_G32 ? s | (((z >> (4 * odd)) & 15u) << 16) : s;
+}
+// in: the block lies inside K (MXFP4's scale code 0 is not 0).
+template <int FMT>
+__device__ __forceinline__ Blk<FMT> unpack_block(u32x4 codes, uint32_t w, bool in) {
+  Blk<FMT> b;
+  b.q = codes;
+  if constexpr (FMT == MOE_W_MXFP4) {
+    b.s0 = in ? e8m0_to_f32(w) : 0.0f;
+    b.s1 = 0.0f;
+  } else if constexpr (FMT == MOE_W_INT4_G32) {
+    b.s0 = (float)bitcast<_Float16>((uint16_t)w);
+    b.s1 = -(float)(w >> 16) * b.s0;
+  } else {
+    b.s0 = e4m3_value(w & 255u);
+    b.s1 = e4m3_value(w >> 8);
+  }
+  return b;
+}
+// A block as loaded from memory, its scale bytes (and the byte of its zero point) not yet converted.
+struct RawBlk {
+  u32x4 q;
+  uint32_t s, z;
+};
+// odd: the block's index is odd (its zero point is the high nibble).  in: it lies inside K.
+template <int FMT>
+__device__ __forceinline__ Blk<FMT> unpack_raw(const RawBlk& r, int odd, bool in) {
+  Blk<FMT> b;
+  b.q = r.q;
+  if constexpr (FMT == MOE_W_MXFP4) {
+    b.s0 = in ? e8m0_to_f32(r.s) : 0.0f;
+    b.s1 = 0.0f;
+  } else {
+    const uint32_t s = in ? r.s : 0u;
+    if constexpr (FMT == MOE_W_INT4_G32) {
+      b.s0 = (float)bitcast<_Float16>((uint16_t)s);
+      b.s1 = -(float)((r.z >> (4 * odd)) & 15u) * b.s0;
+    } else {
+      b.s0 = e4m3_value(s & 255u);
+      b.s1 = e4m3_value(s >> 8);
     }
   }
-  // lane holds rows 4q + i of token l16
+  return b;
+}
+
+// Four consecutive outputs n .. n+3 of token t from their sums.
+template <int FMT>
+__device__ __forceinline__ void store_out(const LinArgs& a, int t, int n, f32x4 v, float ts) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part[wave][m][l16][4 * q + i] = acc[m][i];
-  __syncthreads();
-  const float ts = FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f;
-  for (int i = threadIdx.x; i < MT * 256; i += 256) {
-    const int m = i >> 8, tl = (i >> 4) & 15, r = i & 15;
-    const int t = t0 + 16 * m + tl, row = blockIdx.x * 16 + r;
-    if (t >= a.T || row >= a.N) continue;
-    float v = (part[0][m][tl][r] + part[1][m][tl][r]) + (part[2][m][tl][r] + part[3][m][tl][r]);
-    if constexpr (FMT == MOE_W_NVFP4) v *= ts;
-    if (a.bias) v += a.bias[row];
-    st_value(a.y, a.y_dt, (int64_t)t * a.y_stride + row, v);
+  for (int e = 0; e < 4; ++e) {
+    if (n + e >= a.N) break;
+    float o = v[e];
+    if constexpr (FMT == MOE_W_NVFP4) o *= ts;
+    if (a.bias) o += a.bias[n + e];
+    st_value(a.y, a.y_dt, (int64_t)t * a.y_stride + n + e, o);
   }
 }
 
+// ---- one to four tokens: dot products on the vector ALU ----
+// 8 RG rows per workgroup, whose NW waves share K in spans of 256 values, DP spans in flight each: a lane holds the block lane % 8 of the
+// span of rows lane / 8 + 8 g, so a load instruction takes 8 whole 128-byte lines (nontemporal: used once).  A
+// span of x (512 bytes a token) is loaded as it lies, two tokens per instruction, and passes through LDS of the
+// wave's own to the lanes that need its blocks: loaded in the lanes' order (16 bytes every 64) it took four
+// instructions a token and bound the kernel.  Codes are unpacked to bf16 pairs of small exact integers or E2M1 values, two products per
+// v_dot2_f32_bf16; the block's sum D then takes its scale in fp32:
+//   MXFP4, NVFP4  acc += s D       INT4  acc += s (D - z X), X = the sum of the block's x
+// (an unsigned 4-bit code c as an E4M3 byte is c 2^-9 for every c, so INT4 codes unpack by the 8-bit conversion).
+constexpr int kSpan = 256;
+constexpr int kDotTokens = 4;
+
 template <int FMT>
-void linear_fmt(const LinArgs& a, hipStream_t stream) {
-  const unsigned gn = (unsigned)((a.N + 15) / 16);
-  if (a.T <= 16)
-    linear_rows_kernel<FMT, 1><<<dim3(gn, 1), 256, 0, stream>>>(a);
+struct DotScale {
+  uint32_t s, z;
+};
+
+// Eight codes of dword d as four bf16 pairs (k ascending).
+template <int FMT>
+__device__ __forceinline__ void unpack_pairs(uint32_t d, bf16x2 (&w)[4]) {
+  if constexpr (FMT == MOE_W_INT4_G32) {
+    const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
+    const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
+    w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false);
+    w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true);
+    w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false);
+    w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true);
+  } else {
+    w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
+    w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
+    w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2);
+    w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3);
+  }
+}
+
+template <int FMT, int TT, int RG, int NW, int DP>
+__global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
+  constexpr int XL = (TT + 1) / 2;  // x loads per span
+  __shared__ float red[NW][RG * 8][TT];
+  __shared__ __attribute__((aligned(16))) uint8_t xlds[NW][XL * 1024];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int lr = lane >> 3, lc = lane & 7;
+  const int n0 = blockIdx.x * 8 * RG;
+  const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
+  const int p0 = (int)((int64_t)spans * wave / NW), p1 = (int)((int64_t)spans * (wave + 1) / NW);
+  const int rows = min(8 * RG, a.N - n0);
+  // rows past N fall past the buffer's range and read zeros
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(a.w.w + (int64_t)n0 * a.w.wr, (int64_t)(rows - 1) * a.w.wr + a.K / 2);
+  const uint32_t lbase = (uint32_t)(lr * a.w.wr) + 16u * lc;
+  const uint8_t* srow[RG];
+  const uint8_t* zrow[RG];
+#pragma unroll
+  for (int g = 0; g < RG; ++g) {
+    const int64_t n = n0 + min(8 * g + lr, rows - 1);
+    srow[g] = a.w.s + n * a.w.sr;
+    zrow[g] = FMT == MOE_W_INT4_G32 ? a.w.z + n * a.w.zr : nullptr;
+  }
+  // this lane's part of x: 16-byte piece lane % 32 of the span of token 2 i + lane / 32 (tokens past the last
+  // repeat it; not stored).  Piece i of block b lies at piece i ^ (b / 4) of the block: distinct banks.
+  const int xp = lane & 31;
+  const uint16_t* xrow[XL];
+#pragma unroll
+  for (int i = 0; i < XL; ++i) xrow[i] = a.x + (int64_t)min(2 * i + (lane >> 5), a.T - 1) * a.x_stride;
+  uint8_t* const xw = xlds[wave] + 512 * (lane >> 5) + 64 * (xp >> 2) + 16 * ((xp & 3) ^ (xp >> 4));
+  const uint8_t* const xr = xlds[wave] + 64 * lc;
+  u32x4 codes[DP][RG], x[DP][XL];
+  DotScale<FMT> sc[DP][RG];
+  auto load = [&](int p, u32x4 (&c)[RG], DotScale<FMT> (&s)[RG], u32x4 (&v)[XL]) {
+    const bool in = p < p1 && 8 * p + lc < blocks;
+    const int b = in ? 8 * p + lc : blocks - 1;  // past the wave's share or past K: codes of zero, the rest unused
+#pragma unroll
+    for (int g = 0; g < RG; ++g) c[g] = bld16nt(wr, in ? lbase + (uint32_t)(8 * g * a.w.wr) + 128u * p : kOutOfRange);
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      if constexpr (FMT == MOE_W_MXFP4) {
+        s[g].s = srow[g][b];
+      } else {
+        uint16_t h;
+        __builtin_memcpy(&h, srow[g] + 2 * b, 2);
+        s[g].s = h;
+        if constexpr (FMT == MOE_W_INT4_G32) s[g].z = zrow[g][b >> 1];
+      }
+    }
+    const int k = min(kSpan * p + 8 * xp, a.K - 8);
+#pragma unroll
+    for (int i = 0; i < XL; ++i) v[i] = ld16(xrow[i] + k);
+  };
+#pragma unroll
+  for (int d = 0; d < DP; ++d) load(p0 + d, codes[d], sc[d], x[d]);
+  float acc[RG][TT];
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[g][t] = 0.0f;
+  auto fence = [] {  // LDS operations of one wave stay in program order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  auto span = [&](int p, const u32x4 (&c)[RG], const DotScale<FMT> (&s)[RG], const u32x4 (&xs)[XL]) {
+    const bool in = p < p1 && 8 * p + lc < blocks;
+#pragma unroll
+    for (int i = 0; i < XL; ++i) st16(xw + 1024 * i, xs[i]);
+    fence();
+    u32x4 v[TT][4];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[t][i] = ld16(xr + 512 * t + 16 * (i ^ (lc >> 2)));
+    fence();
+    float X[TT];
+    if constexpr (FMT == MOE_W_INT4_G32) {
+      const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        X[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) X[t] = __builtin_amdgcn_fdot2_f32_bf16(bitcast<bf16x2>(v[t][i >> 2][i & 3]), one, X[t], false);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < RG; ++g) {
+      float D[2][TT];
+#pragma unroll
+      for (int t = 0; t < TT; ++t) D[0][t] = D[1][t] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        bf16x2 w[4];
+        unpack_pairs<FMT>(c[g][i], w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+            D[i >> 1][t] = __builtin_amdgcn_fdot2_f32_bf16(w[k], bitcast<bf16x2>(v[t][i][k]), D[i >> 1][t], false);
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        float o;
+        if constexpr (FMT == MOE_W_MXFP4) {
+          o = e8m0_to_f32(s[g].s) * (D[0][t] + D[1][t]);
+        } else if constexpr (FMT == MOE_W_INT4_G32) {
+          const int b = 8 * p + lc;
+          const float z = (float)((s[g].z >> (4 * (b & 1))) & 15u);
+          o = (float)bitcast<_Float16>((uint16_t)s[g].s) * __builtin_fmaf(-z, X[t], D[0][t] + D[1][t]);
+        } else {
+          o = __builtin_fmaf(e4m3_value(s[g].s & 255u), D[0][t], e4m3_value(s[g].s >> 8) * D[1][t]);
+        }
+        acc[g][t] += in ? o : 0.0f;
+      }
+    }
+  };
+  for (int pb = p0; pb < p1; pb += DP) {
+#pragma unroll
+    for (int d = 0; d < DP; ++d) {
+      span(pb + d, codes[d], sc[d], x[d]);  // (past the wave's share: adds nothing)
+      load(pb + d + DP, codes[d], sc[d], x[d]);
+    }
+  }
+  // over the eight lanes of a row, then over the waves
+#pragma unroll
+  for (int g = 0; g < RG; ++g)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      float v = acc[g][t];
+      v += __shfl_xor(v, 1, kWave);
+      v += __shfl_xor(v, 2, kWave);
+      v += __shfl_xor(v, 4, kWave);
+      if (lc == 0) red[wave][8 * g + lr][t] = v;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < RG * 8 * TT; i += 64 * NW) {
+    const int t = i / (RG * 8), r = i % (RG * 8);
+    if (t >= a.T || r >= rows) continue;
+    float v = red[0][r][t];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[w][r][t];
+    if constexpr (FMT == MOE_W_NVFP4) v *= *a.w.ts;
+    if (a.bias) v += a.bias[n0 + r];
+    st_value(a.y, a.y_dt, (int64_t)t * a.y_stride + n0 + r, v);
+  }
+}
+
+// ---- few tokens: the weights stream once, 16 RT rows per workgroup, its NW waves share K in whole spans ----
+// A span is 256 values of K: 128 bytes of codes per row, so a load instruction (8 rows x 128 bytes) takes whole
+// lines, with the nontemporal hint (a line is used once; the lines of the 16-row x 64-byte shape that the MFMA
+// layout would give read about 13% slower from HBM, and lanes that are neighbours in different rows cost the
+// address unit a cycle each; scale bytes are loaded in the same order for that reason).  A wave keeps DP spans of codes and XP spans of x in flight in
+// registers (one of each serves: eight waves of a CU overlap, and deeper rings measured the same or slower),
+// and turns a span of codes and scales (and half a span of x, 256 bytes a token, four tokens per load) into MFMA
+// layout through LDS of its own.  No load is conditional (registers of loads in flight would be merged, and waited
+// for, at the end of each turn): spans past the wave's share load nothing and add zeros.
+template <int FMT, int RT, int MT, int NW, int DP, int XP>
+__global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
+  constexpr int kWave = RT * 2048 + RT * 512 + MT * 4096;  // LDS bytes of a wave: its span of codes and scales, its half span of x
+  constexpr int kSlots = NW * kWave, kRed = NW * RT * MT * 1024;
+  static_assert(DP % XP == 0, "span d of an unrolled turn uses x set d % XP");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots > kRed ? kSlots : kRed];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l16 = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
+  const int n0 = blockIdx.x * 16 * RT;
+  const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
+  const int p0 = (int)((int64_t)spans * wave / NW), p1 = (int)((int64_t)spans * (wave + 1) / NW);
+  // Buffer descriptors end with the last row's last value.  Only a load's per-lane offset is checked against them,
+  // so that offset holds the row (rows past N and tokens past T lie past the end: zeros) and is put out of range
+  // for a lane past K or past the wave's share; the uniform offset adds the place in K, inside the row for the rest.
+  constexpr int kPer = FMT == MOE_W_MXFP4 ? 1 : 2;  // scale bytes per block
+  const int rows = min(16 * RT, a.N - n0);
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(a.w.w + (int64_t)n0 * a.w.wr, (int64_t)(rows - 1) * a.w.wr + a.K / 2);
+  const __amdgpu_buffer_rsrc_t sr =
+      make_rsrc(a.w.s + (int64_t)n0 * a.w.sr, (int64_t)(rows - 1) * a.w.sr + kPer * blocks);
+  const __amdgpu_buffer_rsrc_t zr =
+      FMT == MOE_W_INT4_G32 ? make_rsrc(a.w.z + (int64_t)n0 * a.w.zr, (int64_t)(rows - 1) * a.w.zr + (blocks + 1) / 2)
+                            : sr;
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, ((int64_t)(a.T - 1) * a.x_stride + a.K) * 2);  // T <= 16 MT
+  const uint32_t woff = (uint32_t)(lr * a.w.wr) + 16u * lc;
+  const uint32_t soff = (uint32_t)(lr * a.w.sr) + kPer * lc, zoff = (uint32_t)(lr * a.w.zr) + (lc >> 1);
+  const uint32_t xoff = (uint32_t)(q * a.x_stride) * 2u + 16u * l16;  // token 4 i + q, piece l16 of a half span
+  u32x4 codes[DP][RT][2], x[XP][2][MT][4];
+  uint32_t sc[DP][RT][2], zp[DP][RT][2];
+  auto load_w = [&](int p, u32x4 (&c)[RT][2], uint32_t (&s)[RT][2], uint32_t (&z)[RT][2]) {
+    const uint32_t out = p < p1 && 8 * p + lc < blocks ? 0u : kOutOfRange;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int row = 16 * r + 8 * g;
+        c[r][g] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (woff + (uint32_t)(row * a.w.wr)) | out, 128u * p, 2));
+        s[r][g] = bld_scale<FMT>(sr, (soff + (uint32_t)(row * a.w.sr)) | out, 8u * kPer * p);
+        z[r][g] = 0;
+        if constexpr (FMT == MOE_W_INT4_G32)
+          z[r][g] = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(row * a.w.zr)) | out, 4u * p, 0);
+      }
+  };
+  auto load_x = [&](int p, u32x4 (&v)[2][MT][4]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t out = p < p1 && kSpan * p + 128 * j + 8 * l16 < a.K ? 0u : kOutOfRange;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[j][m][i] = bld16s(xr, (xoff + (uint32_t)((16 * m + 4 * i) * a.x_stride) * 2u) | out, 512u * p + 256u * j);
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < DP; ++d) load_w(p0 + d, codes[d], sc[d], zp[d]);
+#pragma unroll
+  for (int d = 0; d < XP; ++d) load_x(p0 + d, x[d]);
+  f32x4 acc[RT][MT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint8_t* const slot = lds + wave * kWave;
+  uint32_t* const sslot = reinterpret_cast<uint32_t*>(slot + RT * 2048);  // [16 RT rows][8]: a block's scale bytes
+  uint8_t* const xslot = slot + RT * 2560;
+  auto fence = [] {  // LDS operations of one wave stay in program order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  };
+  for (int pb = p0; pb < p1; pb += DP) {
+#pragma unroll
+    for (int d = 0; d < DP; ++d) {
+      const int p = pb + d;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int w = 8 * g + lr;
+          st16(slot + 2048 * r + 128 * w + 16 * (lc ^ (w >> 1)), codes[d][r][g]);
+          sslot[(16 * r + w) * 8 + lc] = scale_word<FMT>(sc[d][r][g], zp[d][r][g], lc & 1);
+        }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bool in = p < p1 && 8 * p + 4 * j + q < blocks;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            st16(xslot + 4096 * m + 256 * (4 * i + q) + 16 * (l16 ^ (4 * i + q)), x[d % XP][j][m][i]);
+        fence();
+        Blk<FMT> b[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          b[r] = unpack_block<FMT>(ld16(slot + 2048 * r + 128 * l16 + 16 * ((4 * j + q) ^ (l16 >> 1))),
+                                   sslot[(16 * r + l16) * 8 + 4 * j + q], in);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          bf16x8 xf[MT];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+            xf[m] = bitcast<bf16x8>(ld16(xslot + 4096 * m + 256 * l16 + 16 * ((4 * q + k) ^ l16)));
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            bf16x8 lo;
+            const bf16x8 hi = decode<FMT>(b[r], k, lo);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[m], acc[r][m], 0, 0, 0);
+              if constexpr (FMT == MOE_W_INT4_G32)
+                acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[m], acc[r][m], 0, 0, 0);
+            }
+          }
+        }
+        fence();
+      }
+      load_w(p + DP, codes[d], sc[d], zp[d]);
+      load_x(p + XP, x[d % XP]);
+      __builtin_amdgcn_sched_barrier(0);  // (a later span's waits stay behind this one's loads)
+    }
+  }
+  // the waves' sums: [wave][r][m][lane] as four rows of one token
+  __syncthreads();
+  f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) red[((wave * RT + r) * MT + m) * 64 + lane] = acc[r][m];
+  __syncthreads();
+  const float ts = FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f;
+  for (int i = threadIdx.x; i < RT * MT * 64; i += 64 * NW) {
+    f32x4 v = red[i];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) v += red[w * RT * MT * 64 + i];
+    const int l = i & 63, m = (i >> 6) % MT, r = i / (64 * MT);
+    const int t = 16 * m + (l & 15), n = n0 + 16 * r + 4 * (l >> 4);
+    if (t < a.T) store_out<FMT>(a, t, n, v, ts);
+  }
+}
+
+// ---- many tokens: tiles of 128 rows of W x 32 MTW tokens, four waves of 64 rows x 16 MTW tokens ----
+// A step is 128 values of K.  Its x (256 bytes per token) goes through a two-stage LDS ring, loaded into registers
+// PD steps ahead; 16-byte piece p of token t lies at piece p ^ (t % 16), so that the 16 tokens of an MFMA operand
+// read distinct banks.  Weights never touch LDS: a lane loads its row's block (16 bytes) in MFMA layout PD steps
+// ahead and decodes it in registers (twice per workgroup, since two waves share a row: 4 conversions per MFMA
+// operand that then serves MTW instructions).  With few tiles the workgroups of a tile share K (splits) and leave
+// fp32 partial sums, which linear_join_kernel adds in order.
+constexpr int kStep = 128;
+
+template <int DT>
+__device__ __forceinline__ void store4(const LinArgs& a, int t, int n, f32x4 v, bool vec) {
+  typename Val<DT>::S* d = reinterpret_cast<typename Val<DT>::S*>(a.y) + (int64_t)t * a.y_stride + n;
+  if (vec && n + 4 <= a.N) {
+    if constexpr (DT == MOE_DT_FP32)
+      *reinterpret_cast<f32x4*>(d) = v;
+    else
+      *reinterpret_cast<u32x2*>(d) = u32x2{(uint32_t)f32_to_16(v[0], DT) | ((uint32_t)f32_to_16(v[1], DT) << 16),
+                                           (uint32_t)f32_to_16(v[2], DT) | ((uint32_t)f32_to_16(v[3], DT) << 16)};
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (n + e < a.N) {
+      if constexpr (DT == MOE_DT_FP32)
+        d[e] = v[e];
+      else
+        d[e] = f32_to_16(v[e], DT);
+    }
+}
+
+// A wave's outputs: rows n + 16 r + i of token t + 16 m from acc[r][m][i].
+template <int FMT, int MTW, int DT>
+__device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f32x4 (&acc)[4][MTW],
+                                         const f32x4 (&bias)[4], float ts, bool vec) {
+#pragma unroll
+  for (int m = 0; m < MTW; ++m)
+    if (t + 16 * m < a.T) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        f32x4 v = acc[r][m];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = FMT == MOE_W_NVFP4 ? __builtin_fmaf(v[e], ts, bias[r][e]) : v[e] + bias[r][e];
+        store4<DT>(a, t + 16 * m, n + 16 * r, v, vec);
+      }
+    }
+}
+
+template <int FMT, int MTW, int PD>
+__global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_tiles, int n_tiles, int splits) {
+  constexpr int kTok = 32 * MTW, kStage = kTok * 256;  // tokens, LDS bytes of a stage
+  constexpr int kXL = kStage / 16 / 256;               // 16-byte pieces of x per thread and step
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int l16 = lane & 15, q = lane >> 4;
+  const int split = blockIdx.x / (t_tiles * n_tiles), tile = blockIdx.x % (t_tiles * n_tiles);
+  const int t0 = (tile % t_tiles) * kTok, nw = (tile / t_tiles) * 128 + (wave >> 1) * 64;
+  const int tw = (wave & 1) * 16 * MTW;  // the wave's first token in the tile
+  // K in turns of PD steps (the last one may pass the end of K)
+  const int blocks = a.K / 32, turns = (a.K + PD * kStep - 1) / (PD * kStep);
+  const int k0 = PD * (int)((int64_t)turns * split / splits), k1 = PD * (int)((int64_t)turns * (split + 1) / splits);
+
+  // As in the streaming kernel, a load's per-lane offset holds the row and is checked (rows past N and tokens past
+  // T read zeros; so does a lane past K), the uniform offset adds the place in K.  No load is conditional: the
+  // registers of loads in flight would be merged, and waited for, at the end of each turn.
+  constexpr int kPer = FMT == MOE_W_MXFP4 ? 1 : 2;  // scale bytes per block
+  const int rows = max(0, min(64, a.N - nw)), toks = min(kTok, a.T - t0);
+  const __amdgpu_buffer_rsrc_t wr =
+      make_rsrc(a.w.w + (int64_t)nw * a.w.wr, rows ? (int64_t)(rows - 1) * a.w.wr + a.K / 2 : 0);
+  const __amdgpu_buffer_rsrc_t sr =
+      make_rsrc(a.w.s + (int64_t)nw * a.w.sr, rows ? (int64_t)(rows - 1) * a.w.sr + kPer * blocks : 0);
+  const __amdgpu_buffer_rsrc_t zr =
+      FMT == MOE_W_INT4_G32
+          ? make_rsrc(a.w.z + (int64_t)nw * a.w.zr, rows ? (int64_t)(rows - 1) * a.w.zr + (blocks + 1) / 2 : 0)
+          : sr;
+  const __amdgpu_buffer_rsrc_t xr =
+      make_rsrc(a.x + (int64_t)t0 * a.x_stride, ((int64_t)(toks - 1) * a.x_stride + a.K) * 2);
+  const uint32_t woff = (uint32_t)(l16 * a.w.wr) + 16u * q, soff = (uint32_t)(l16 * a.w.sr) + kPer * q;
+  const uint32_t zoff = (uint32_t)(l16 * a.w.zr) + (q >> 1);
+  const uint32_t xoff = (uint32_t)((threadIdx.x >> 4) * a.x_stride) * 2u + 16u * (threadIdx.x & 15);
+  auto load_w = [&](int k, RawBlk (&w)[4]) {
+    const uint32_t out = 4 * k + q < blocks ? 0u : kOutOfRange;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      w[r].q = bld16s(wr, (woff + (uint32_t)(16 * r * a.w.wr)) | out, 64u * k);
+      w[r].s = bld_scale<FMT>(sr, (soff + (uint32_t)(16 * r * a.w.sr)) | out, 4u * kPer * k);
+      w[r].z = 0;
+      if constexpr (FMT == MOE_W_INT4_G32)
+        w[r].z = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(16 * r * a.w.zr)) | out, 2u * k, 0);
+    }
+  };
+  auto load_x = [&](int k, u32x4 (&x)[kXL]) {
+    const uint32_t out = kStep * k + 8 * (int)(threadIdx.x & 15) < a.K ? 0u : kOutOfRange;
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) x[i] = bld16s(xr, (xoff + (uint32_t)(16 * i * a.x_stride) * 2u) | out, 256u * k);
+  };
+  auto put_x = [&](int stage, const u32x4 (&x)[kXL]) {
+#pragma unroll
+    for (int i = 0; i < kXL; ++i) {
+      const int f = threadIdx.x + 256 * i, t = f >> 4, c = f & 15;
+      st16(lds + stage * kStage + 256 * t + 16 * (c ^ (t & 15)), x[i]);
+    }
+  };
+  f32x4 acc[4][MTW];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int m = 0; m < MTW; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+  static_assert(PD % 2 == 0, "the LDS stage of an unrolled step is fixed");
+  RawBlk w[PD][4];
+  u32x4 x[PD][kXL];  // x of step k in set k % PD (counted from k0)
+#pragma unroll
+  for (int d = 0; d < PD; ++d) {
+    load_w(k0 + d, w[d]);
+    load_x(k0 + d, x[d]);
+  }
+  put_x(0, x[0]);
+  load_x(k0 + PD, x[0]);
+  __syncthreads();
+  for (int kb = k0; kb < k1; kb += PD) {
+#pragma unroll
+    for (int d = 0; d < PD; ++d) {
+      const int k = kb + d;
+      const int stage = d & 1;
+      const bool in = 4 * k + q < blocks;  // (MXFP4: scale code 0 is not 0)
+      Blk<FMT> b[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) b[r] = unpack_raw<FMT>(w[d][r], q & 1, in);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        bf16x8 xf[MTW];
+#pragma unroll
+        for (int m = 0; m < MTW; ++m)
+          xf[m] = bitcast<bf16x8>(ld16(lds + stage * kStage + 256 * (tw + 16 * m + l16) + 16 * ((4 * q + s) ^ l16)));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          bf16x8 lo;
+          const bf16x8 hi = decode<FMT>(b[r], s, lo);
+#pragma unroll
+          for (int m = 0; m < MTW; ++m) {
+            acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[m], acc[r][m], 0, 0, 0);
+            if constexpr (FMT == MOE_W_INT4_G32)
+              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[m], acc[r][m], 0, 0, 0);
+          }
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);  // the waits for the next step's x stay behind the products
+      put_x(stage ^ 1, x[(d + 1) % PD]);
+      load_w(k + PD, w[d]);
+      load_x(k + 1 + PD, x[(d + 1) % PD]);
+      __syncthreads();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // lane: rows 4q + i of row tile r, token l16 of token tile m
+  f32x4 bias[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = nw + 16 * r + 4 * q + e;
+      bias[r][e] = a.bias && splits == 1 && n < a.N ? a.bias[n] : 0.0f;
+    }
+  const float ts = FMT == MOE_W_NVFP4 && splits == 1 ? *a.w.ts : 1.0f;
+  if (splits > 1) {
+    LinArgs o = a;
+    o.y = reinterpret_cast<float*>(a.ws) + (int64_t)split * a.T * a.N;
+    o.y_stride = a.N;
+    tile_out<FMT, MTW, MOE_DT_FP32>(o, t0 + tw + l16, nw + 4 * q, acc, bias, ts, a.N % 4 == 0);
+    return;
+  }
+  const bool vec = a.y_stride % 4 == 0 && ((uintptr_t)a.y & (a.y_dt == MOE_DT_FP32 ? 15u : 7u)) == 0;
+  if (a.y_dt == MOE_DT_FP32) tile_out<FMT, MTW, MOE_DT_FP32>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+  else if (a.y_dt == MOE_DT_BF16) tile_out<FMT, MTW, MOE_DT_BF16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+  else tile_out<FMT, MTW, MOE_DT_FP16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+}
+
+// y = the partial sums of the splits in order, with the tensor scale and the bias.
+template <int FMT>
+__global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int n4 = (a.N + 3) / 4;
+  if (i >= (int64_t)a.T * n4) return;
+  const int t = (int)(i / n4), n = (int)(i % n4) * 4;
+  const float* p = reinterpret_cast<const float*>(a.ws) + (int64_t)t * a.N + n;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s, p += (int64_t)a.T * a.N)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < a.N) v[e] += p[e];
+  store_out<FMT>(a, t, n, v, FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f);
+}
+
+// Eight rows per workgroup; eight waves where the rows give at most a workgroup per CU (one token, 1000 x 2080
+// INT4 3.2 against 3.3 us with four waves, 512 x 7168 NVFP4 4.2 against 5.5), four beyond (7168 x 7168 MXFP4 7.9
+// against 9.2).  Two spans in flight: four measured the same or slower.
+template <int FMT, int TT>
+void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
+  const dim3 g((unsigned)((a.N + 7) / 8));
+  if (a.N <= 2048) linear_dot_kernel<FMT, TT, 1, 8, 2><<<g, 512, 0, stream>>>(a);
+  else linear_dot_kernel<FMT, TT, 1, 4, 2><<<g, 256, 0, stream>>>(a);
+}
+
+// Rows per workgroup: every workgroup reads all of x, so as many as leave about 200 workgroups (one per CU).  16
+// tokens, 7168 rows x 7168: 16 rows 14.5 us, 32 rows 12.6; 2048 rows: 8.3 and 11.1; 32 tokens, 16384 rows x 4096:
+// 33.5, 20.4 and 64 rows 17.3.  Eight waves, four where their LDS does not fit (64 tokens and more than 16 rows).
+template <int FMT, int MT, int RT>
+void launch_stream_rows(const LinArgs& a, hipStream_t stream) {
+  constexpr int NW = MT == 4 && RT > 1 ? 4 : 8;
+  linear_stream_kernel<FMT, RT, MT, NW, 1, 1><<<dim3((unsigned)((a.N + 16 * RT - 1) / (16 * RT))), 64 * NW, 0, stream>>>(a);
+}
+template <int FMT, int MT>
+void launch_stream_tokens(const LinArgs& a, hipStream_t stream) {
+  if (a.N >= 64 * 200) launch_stream_rows<FMT, MT, 4>(a, stream);
+  else if (a.N >= 32 * 200) launch_stream_rows<FMT, MT, 2>(a, stream);
+  else launch_stream_rows<FMT, MT, 1>(a, stream);
+}
+
+constexpr int kStreamTokens = 64;  // at most this many tokens stream the weights
+
+// Tiles and K shares of the tile kernel: 64-token tiles where 128 would leave half of the tile empty; K shared
+// until there are two workgroups per CU, at least four steps each.
+struct TilePlan {
+  int mtw, t_tiles, n_tiles, splits;
+};
+TilePlan tile_plan(int T, int N, int K) {
+  TilePlan p;
+  p.mtw = (T + 127) / 128 * 128 - T >= 64 ? 2 : 4;
+  p.t_tiles = (T + 32 * p.mtw - 1) / (32 * p.mtw);
+  p.n_tiles = (N + 127) / 128;
+  const int64_t tiles = (int64_t)p.t_tiles * p.n_tiles;
+  const int64_t most = std::min<int64_t>(8, std::max(1, K / (4 * kStep)));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / tiles));
+  return p;
+}
+
+template <int FMT>
+hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
+  if (a.T <= kStreamTokens) {
+    if (a.T == 1) launch_dot_tokens<FMT, 1>(a, stream);
+    else if (a.T == 2) launch_dot_tokens<FMT, 2>(a, stream);
+    else if (a.T <= kDotTokens) launch_dot_tokens<FMT, 4>(a, stream);
+    else if (a.T <= 16) launch_stream_tokens<FMT, 1>(a, stream);
+    else if (a.T <= 32) launch_stream_tokens<FMT, 2>(a, stream);
+    else launch_stream_tokens<FMT, 4>(a, stream);
+    return hipGetLastError();
+  }
+  const TilePlan p = tile_plan(a.T, a.N, a.K);
+  const int64_t g = (int64_t)p.t_tiles * p.n_tiles * p.splits;
+  if (g > 0x7FFFFF) return hipErrorInvalidConfiguration;  // (more than 2^31 threads)
+  if (p.mtw == 2)
+    linear_tile_kernel<FMT, 2, 2><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
   else
-    linear_rows_kernel<FMT, 4><<<dim3(gn, (unsigned)((a.T + 63) / 64)), 256, 0, stream>>>(a);
+    linear_tile_kernel<FMT, 4, 2><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.splits == 1) return err;
+  const int64_t n = (int64_t)a.T * ((a.N + 3) / 4);
+  linear_join_kernel<FMT><<<dim3((unsigned)((n + 255) / 256)), 256, 0, stream>>>(a, p.splits);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-size_t linear_workspace_bytes(int T, int fmt, int N, int K) {
-  (void)T, (void)fmt, (void)N, (void)K;
-  return 0;
+size_t linear_workspace_bytes(int T, int N, int K) {
+  if (T <= kStreamTokens) return 0;
+  const TilePlan p = tile_plan(T, N, K);
+  return p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)T * (size_t)N : 0;
 }
 
 hipError_t launch_linear(const LinArgs& a, hipStream_t stream) {
-  if (a.fmt == MOE_W_MXFP4) linear_fmt<MOE_W_MXFP4>(a, stream);
-  else if (a.fmt == MOE_W_INT4_G32) linear_fmt<MOE_W_INT4_G32>(a, stream);
-  else linear_fmt<MOE_W_NVFP4>(a, stream);
-  return hipGetLastError();
+  if (a.fmt == MOE_W_MXFP4) return linear_fmt<MOE_W_MXFP4>(a, stream);
+  if (a.fmt == MOE_W_INT4_G32) return linear_fmt<MOE_W_INT4_G32>(a, stream);
+  return linear_fmt<MOE_W_NVFP4>(a, stream);
 }
 
 }  // namespace moe

@@ -122,7 +122,7 @@ def test_linear_refusals(fmt):
     assert L.moe_linear(None, 0, 0, 0, None, None, None, 0, 0, None, 0, None) == OK
     assert L.moe_linear(fake(), 0, 64, 4, None, None, fake(), 2, 32, None, 0, None) == NULL
     assert f(x=None) == NULL and f(y=None) == NULL and f(D(w=None)) == NULL and f(D(scales=None)) == NULL
-    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
+    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62), dict(d=D(s_row_stride=1 << 25)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
                 dict(d=D(w_row_stride=16)), dict(d=D(s_row_stride=1)), dict(d=D(w_row_stride=1 << 25))):
         assert f(**bad) == SHAPE, bad
     assert f(D(k_in=48)) == BLOCK and f(D(w=P + 8)) == BLOCK and f(D(w_row_stride=40)) == BLOCK
@@ -132,6 +132,12 @@ def test_linear_refusals(fmt):
         assert f(D(zeros=None)) == NULL and f(D(z_row_stride=0)) == SHAPE
     if fmt == m.MOE_W_NVFP4:
         assert f(D(tensor_scale=None)) == NULL and f(D(tensor_scale=P + 2)) == ALIGN
+    assert L.moe_linear_workspace_bytes(4, ctypes.byref(D())) == 0
+    wide = D(k_in=4096, w_row_stride=2048, s_row_stride=256, **({"z_row_stride": 64} if fmt == m.MOE_W_INT4_G32 else {}))
+    need = L.moe_linear_workspace_bytes(200, ctypes.byref(wide))
+    assert need >= 4 * 200 * 32
+    assert f(wide, T=200, xs=4096, ws=None) == WORKSPACE and f(wide, T=200, xs=4096, wsb=need - 1) == WORKSPACE
+    assert f(wide, T=200, xs=4096, ws=fake(0x8008)) == ALIGN
     assert L.moe_linear_workspace_bytes(4, None) == 0 and L.moe_linear_workspace_bytes(0, ctypes.byref(D())) == 0
 
 

@@ -97,6 +97,39 @@ def test_slices(fmt, T):
         assert np.all(np.abs(got - want) <= ref.linear_tolerance(x, ww, k1 - k0, want, "fp32"))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,N", [(1, 2100), (3, 2049), (7, 6437), (9, 12850), (20, 6437), (25, 12850), (40, 6437),
+                                 (50, 12850), (90, 6437), (700, 1030)])
+def test_many_rows(fmt, T, N):
+    check(T, N, 288, fmt, "bf16", bias=True)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 3, 12, 30, 60, 150])
+def test_scales_at_any_address(fmt, T):
+    """Scale and zero-point rows at odd addresses, an odd number of bytes apart."""
+    rng = np.random.default_rng(8)
+    N, K = 50, 544
+    codes, scales, zeros, ts, w = ref.weights(fmt, N, K, rng)
+
+    def odd(a):
+        if a is None:
+            return None
+        width = a.shape[1] + (2 if a.shape[1] % 2 else 1)
+        buf = torch.zeros(1 + N * width, dtype=torch.uint8, device=DEV)
+        view = buf[1:].view(N, width)[:, :a.shape[1]]
+        view.copy_(dev(a))
+        return view
+
+    S, Z = odd(scales), odd(zeros)
+    assert S.data_ptr() % 2 == 1 and S.stride(0) % 2 == 1
+    X = torch.from_numpy(rng.standard_normal((T, K))).bfloat16()
+    x = X.double().numpy()
+    want = x @ w.T
+    got = moe.moe_linear(X.to(DEV), moe.LinearWeights(dev(codes), S, fmt, Z, dev(ts))).double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= ref.linear_tolerance(x, w, K, want, "fp32"))
+
+
 @pytest.mark.parametrize("T", [1, 20, 150])
 def test_extreme_scales(T):
     """MXFP4 scale codes from the smallest to those whose sums fill fp32."""
