@@ -122,6 +122,23 @@ def test_keys_closer_than_fp32():
     check(L, top_k=12, score="sigmoid", bias=torch.zeros(64))
 
 
+def test_many_close_keys():
+    """More close keys than lanes of a wave, around the last slot and among many slots."""
+    for dtype in ("bf16", "fp32"):
+        L = logits(3, 512, dtype, seed=6, std=0.01 if dtype == "bf16" else 1.0)
+        if dtype == "fp32":
+            L = L.mul(2.0 ** -22).add(0.75)  # a few hundred neighbours
+        for score in ("softmax", "sigmoid"):
+            for k in (4, 62, 63, 64, 130):
+                check(L, top_k=k, score=score, bias=torch.zeros(512))
+            check(L, top_k=9, score=score, bias=torch.full((512,), -0.5), n_groups=4, topk_groups=2, group_score="max")
+    same = torch.zeros(2, 256)
+    for k in (1, 8, 63, 64, 200):
+        check(same, top_k=k, score="sigmoid", bias=torch.full((256,), 0.25))
+    check(logits(5, 700, seed=3), top_k=120, score="sigmoid", bias=bias_of(700))
+    check(logits(5, 700, seed=3), top_k=120, bias=bias_of(700, 1e-3), n_groups=7, topk_groups=3)
+
+
 def test_wide_logits():
     """Scores over the whole range of fp32, and keys under a large bias."""
     for std in (5.0, 40.0):
