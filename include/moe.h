@@ -448,7 +448,7 @@ moe_status moe_expert_ffn_mx_codes(const uint8_t *x_codes, const uint8_t *x_scal
  *       that is not checked)
  *   y       [T][hidden], aligned to a value, or NULL
  *   codes   [T] packed rows (moe_mx_row_bytes), 16-byte aligned; scales [T][hidden/32]; fmt 0: both NULL
- * Rows of 16-byte aligned pointers and strides with hidden a multiple of 8, up to 32768, take the fast kernels.
+ * Rows of 8 to 32768 values take the fast kernels.
  * Errors: NULL (also neither y nor codes wanted, residual_out without residual), SHAPE (T<0, hidden<1, a stride
  * below hidden, eps negative or not finite), BLOCK (codes with hidden % 32), DTYPE, ALIGN, HIP. */
 typedef struct {

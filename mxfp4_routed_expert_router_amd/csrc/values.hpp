@@ -23,7 +23,8 @@ struct Val<MOE_DT_FP32> {
   static __device__ __forceinline__ float get(S v) { return v; }
 };
 
-// Eight consecutive values as they are stored (16 or 32 bytes), and their fp32 values.
+// Eight consecutive values as they are stored (16 or 32 bytes), and their fp32 values.  The addresses need a
+// value's alignment only: gfx950 takes 16-byte global accesses at any address.
 template <int DT>
 struct Raw8 {
   u32x4 q[DT == MOE_DT_FP32 ? 2 : 1];
@@ -31,9 +32,7 @@ struct Raw8 {
 template <int DT>
 __device__ __forceinline__ Raw8<DT> ld_raw8(const void* p, int64_t i) {  // i: index of the first value
   Raw8<DT> r;
-  const u32x4* s = reinterpret_cast<const u32x4*>(reinterpret_cast<const typename Val<DT>::S*>(p) + i);
-  r.q[0] = s[0];
-  if constexpr (DT == MOE_DT_FP32) r.q[1] = s[1];
+  __builtin_memcpy(&r, reinterpret_cast<const typename Val<DT>::S*>(p) + i, sizeof(r));
   return r;
 }
 template <int DT>
@@ -47,7 +46,7 @@ __device__ __forceinline__ void raw8_to_f32(const Raw8<DT>& r, float (&v)[8]) {
   }
 }
 
-// Run-time storage type: one value, or eight values of a 16-byte aligned run.
+// Run-time storage type: one value, or eight consecutive ones.
 __device__ __forceinline__ float ld_value(const void* p, int dt, int64_t i) {
   if (dt == MOE_DT_FP32) return reinterpret_cast<const float*>(p)[i];
   const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
@@ -66,14 +65,13 @@ template <int DT>
 __device__ __forceinline__ void st8_as(void* p, int64_t i, const float (&v)[8]) {
   typename Val<DT>::S* d = reinterpret_cast<typename Val<DT>::S*>(p) + i;
   if constexpr (DT == MOE_DT_FP32) {
-    *reinterpret_cast<f32x4*>(d) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(d + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    __builtin_memcpy(d, v, 32);
   } else {
     u32x4 q;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       q[j] = (uint32_t)f32_to_16(v[2 * j], DT) | ((uint32_t)f32_to_16(v[2 * j + 1], DT) << 16);
-    st16(d, q);
+    __builtin_memcpy(d, &q, 16);
   }
 }
 __device__ __forceinline__ void st8(void* p, int dt, int64_t i, const float (&v)[8]) {

@@ -93,6 +93,14 @@ def test_in_place_and_strided(H, pad, mx):
     check(5, H, "bf16", "bf16", "bf16", "bf16", mx, seed=pad, pad=pad, in_place=True)
 
 
+@pytest.mark.parametrize("H", [5, 9, 63, 257, 513, 4097, 8191, 16411, 32769])
+@pytest.mark.parametrize("pad", [0, 2])
+def test_in_place_odd(H, pad):
+    """The last run of a row overlaps the one before: in place, no value may be added twice."""
+    check(3, H, "fp16", "fp16", "fp16", "bf16", None, seed=H, pad=pad, in_place=True)
+    check(2, H, "bf16", "fp32", "fp32", "fp32", None, seed=H, pad=pad, in_place=True)
+
+
 @pytest.mark.parametrize("H", [512, 513])
 def test_scales_of_values(H):
     check(4, H, "fp32", "fp32", "fp32", "fp32", None, scale=1e-12, eps=1e-30)
