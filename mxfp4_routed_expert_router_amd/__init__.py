@@ -543,21 +543,20 @@ def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: Ex
 
 
 # ----------------------------------------------------------------------------------------------------
-# In front of the layer.  These calls run once per layer and token, with few microseconds of GPU time at small T:
-# the descriptions are built once, and a call passes plain integers.
+# In front of the layer.  These calls take few microseconds of GPU time at small T: descriptions are built once, a
+# call checks what its pointers cannot tell and passes plain integers.
 def _dense(what: str, t: torch.Tensor, dtype, shape) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
 
 
-def _rows(what: str, t: torch.Tensor, width: int, device=None) -> int:
-    """Row stride (in values) of a [T][width] tensor whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != width or (t.stride(1) != 1 and width > 1):
-        raise ValueError(f"{what} must be [T][{width}] with contiguous rows, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+def _rows(what: str, t: torch.Tensor, T: int, width: int, index: Optional[int]) -> int:
+    """Row stride (in values) of a [T][width] tensor with contiguous rows on GPU `index`."""
+    if t.shape != (T, width) or (t.stride(1) != 1 and width > 1) or t.device.index != index:
+        raise ValueError(f"{what} must be [{T}][{width}] with contiguous rows on GPU {index}, got {tuple(t.shape)} on "
+                         f"{t.device}")
+    return t.stride(0) if T > 1 else width
 
 
 def _dtype(what: str, t: torch.Tensor) -> int:
@@ -567,25 +566,23 @@ def _dtype(what: str, t: torch.Tensor) -> int:
     return d
 
 
-class _on:
-    """The tensor's device made current for a call, and its current stream."""
+def _gpu(t: torch.Tensor) -> int:
+    index = t.device.index
+    if index is None or not t.is_cuda:
+        raise ValueError(f"needs a GPU tensor, got one on {t.device}")
+    return index
 
-    __slots__ = ("index", "before")
 
-    def __init__(self, device: torch.device):
-        if device.type != "cuda":
-            raise ValueError(f"needs a GPU tensor, got one on {device}")
-        self.index = device.index
-
-    def __enter__(self) -> int:
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc) -> None:
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+def _enqueue(name: str, index: int, *args) -> None:
+    """Calls the library on GPU `index` and its current stream (the last argument)."""
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
+        _check(status, name)
 
 
 class RouteRule:
@@ -599,7 +596,7 @@ class RouteRule:
                  routed_scale: float = 1.0, n_shared: int = 0, shared_weight: float = 1.0):
         if selection_bias is not None:
             _dense("RouteRule: selection_bias", selection_bias, torch.float32, (selection_bias.numel(),))
-        self.selection_bias, self.top_k, self.n_shared = selection_bias, top_k, n_shared
+        self.selection_bias, self.top_k, self.n_shared, self.k_total = selection_bias, top_k, n_shared, top_k + n_shared
         self.c = moe_route_rule(SCORES[score], top_k, n_shared, n_groups, topk_groups, GROUP_SCORES[group_score],
                                 int(bool(renormalise)), routed_scale, shared_weight,
                                 None if selection_bias is None else selection_bias.data_ptr())
@@ -610,7 +607,7 @@ def _route_out(what: str, rule: RouteRule, T: int, E: int, dev, want_scores: boo
     b = rule.selection_bias
     if b is not None and (b.numel() != E or b.device != dev):
         raise ValueError(f"{what}: the selection bias has {b.numel()} values on {b.device}, expected {E} on {dev}")
-    kt = rule.top_k + rule.n_shared
+    kt = rule.k_total
     if out is None:
         return (torch.empty((T, kt), dtype=torch.int32, device=dev),
                 torch.empty((T, kt), dtype=torch.float32, device=dev),
@@ -627,13 +624,11 @@ def moe_select_experts(logits: torch.Tensor, rule: RouteRule, want_scores: bool 
     """The rule on router logits [T][E] (bf16, fp16 or fp32, contiguous rows)
     -> (ids int32 [T][k'], weights fp32 [T][k'], scores fp32 [T][E] or None)."""
     T, E = logits.shape
-    dev = logits.device
-    ids, w, scores = _route_out("moe_select_experts", rule, T, E, dev, want_scores, out)
-    stride = _rows("moe_select_experts: logits", logits, E)
-    with _on(dev) as stream:
-        _check(lib().moe_select_experts(logits.data_ptr(), _dtype("logits", logits), stride, T, E, rule.at,
-                                        ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
-                                        stream), "moe_select_experts")
+    gpu = _gpu(logits)
+    stride = _rows("moe_select_experts: logits", logits, T, E, gpu)
+    ids, w, scores = _route_out("moe_select_experts", rule, T, E, logits.device, want_scores, out)
+    _enqueue("moe_select_experts", gpu, logits.data_ptr(), _dtype("logits", logits), stride, T, E, rule.at,
+             ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr())
     return ids, w, scores
 
 
@@ -643,15 +638,14 @@ def moe_route_grouped(x: torch.Tensor, w_router: torch.Tensor, rule: RouteRule, 
     T, H = x.shape
     E = w_router.shape[0]
     dev = x.device
+    gpu = _gpu(x)
     _dense("moe_route_grouped: x", x, x.dtype, (T, H))
     _dense("moe_route_grouped: w_router", w_router, torch.float32, (E, H))
     ids, w, scores = _route_out("moe_route_grouped", rule, T, E, dev, want_scores, out)
     ws = workspace if workspace is not None else _workspace(moe_route_workspace_bytes(T, H, E), dev)
-    with _on(dev) as stream:
-        _check(lib().moe_route_grouped(x.data_ptr(), _act_dtype(x), T, H, w_router.data_ptr(), E, rule.at,
-                                       ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
-                                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                                       stream), "moe_route_grouped")
+    _enqueue("moe_route_grouped", gpu, x.data_ptr(), _act_dtype(x), T, H, w_router.data_ptr(), E, rule.at,
+             ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
+             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
     return ids, w, scores
 
 
@@ -673,17 +667,19 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
     out (None without).  `out` gives the four buffers; a None for y or residual_out there leaves that output
     out, and residual_out may be residual itself."""
     T, H = x.shape
-    dev = x.device
+    gpu = _gpu(x)
     f = 0 if mx is None else _mx_fmt(mx)
-    if norm.weight.device != dev:
-        raise ValueError(f"moe_add_rms_norm: the weight is on {norm.weight.device}, x on {dev}")
-    xs = _rows("moe_add_rms_norm: x", x, norm.hidden)
+    if norm.hidden != H or norm.weight.device.index != gpu:
+        raise ValueError(f"moe_add_rms_norm: rows of {H} values on GPU {gpu}, the weight has {norm.hidden} on "
+                         f"{norm.weight.device}")
+    xs = _rows("moe_add_rms_norm: x", x, T, H, gpu)
+    rp = rop = cp = sp = None
     rs = ros = rdt = 0
     if residual is not None:
-        rs, rdt = _rows("moe_add_rms_norm: residual", residual, H, dev), _dtype("residual", residual)
-        if residual.shape[0] != T:
-            raise ValueError(f"moe_add_rms_norm: {T} rows of x, {residual.shape[0]} of the residual")
+        rs, rdt, rp = (_rows("moe_add_rms_norm: residual", residual, T, H, gpu), _dtype("residual", residual),
+                       residual.data_ptr())
     if out is None:
+        dev = x.device
         y = torch.empty((T, H), dtype=dtype, device=dev)
         ro = None if residual is None else torch.empty((T, H), dtype=residual.dtype, device=dev)
         codes = scales = None
@@ -695,18 +691,18 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
         if y is not None:
             _dense("moe_add_rms_norm: y", y, y.dtype, (T, H))
         if f:
-            _dense("moe_add_rms_norm: codes", codes, torch.uint8, (T, moe_mx_row_bytes(f, H)))
+            if codes is None or scales is None:
+                raise ValueError("moe_add_rms_norm: mx needs codes and scales")
+            _dense("moe_add_rms_norm: codes", codes, torch.uint8, (T, H if f == MOE_MX_FP8_E4M3 else moe_mx_row_bytes(f, H)))
             _dense("moe_add_rms_norm: scales", scales, torch.uint8, (T, H // 32))
-        if ro is not None and (residual is None or ro.dtype != residual.dtype or ro.shape[0] != T):
-            raise ValueError("moe_add_rms_norm: residual_out needs a residual of its type and rows")
+        if ro is not None and (residual is None or ro.dtype is not residual.dtype):
+            raise ValueError("moe_add_rms_norm: residual_out needs a residual of its type")
     if ro is not None:
-        ros = _rows("moe_add_rms_norm: residual_out", ro, H, dev)
-    with _on(dev) as stream:
-        _check(lib().moe_add_rms_norm(norm.at, x.data_ptr(), _dtype("x", x), xs,
-                                      None if residual is None else residual.data_ptr(), rdt, rs, T,
-                                      None if ro is None else ro.data_ptr(), ros, None if y is None else y.data_ptr(),
-                                      0 if y is None else _dtype("y", y), f, None if codes is None else codes.data_ptr(),
-                                      None if scales is None else scales.data_ptr(), stream), "moe_add_rms_norm")
+        ros, rop = _rows("moe_add_rms_norm: residual_out", ro, T, H, gpu), ro.data_ptr()
+    if f:
+        cp, sp = codes.data_ptr(), scales.data_ptr()
+    _enqueue("moe_add_rms_norm", gpu, norm.at, x.data_ptr(), _dtype("x", x), xs, rp, rdt, rs, T, rop, ros,
+             None if y is None else y.data_ptr(), 0 if y is None else _dtype("y", y), f, cp, sp)
     return y, ro, codes, scales
 
 
@@ -724,7 +720,7 @@ class LinearWeights:
         def rows(what, t, width):
             if t is None or t.dtype != torch.uint8 or t.shape[0] != self.n_out or t.device != codes.device:
                 raise ValueError(f"LinearWeights: {what} must be uint8 [{self.n_out}][{width}] on {codes.device}")
-            return t.data_ptr(), _rows(f"LinearWeights: {what}", t, width)
+            return t.data_ptr(), _rows(f"LinearWeights: {what}", t, self.n_out, width, codes.device.index)
 
         p.w, p.w_row_stride = rows("codes", codes, K // 2)
         p.scales, p.s_row_stride = rows("scales", scales, K // 32 if self.fmt == MOE_W_MXFP4 else K // 16)
@@ -736,13 +732,17 @@ class LinearWeights:
             _dense("LinearWeights: tensor_scale", tensor_scale, torch.float32, (1,))
             p.tensor_scale = tensor_scale.data_ptr()
         self.tensors = (codes, scales, zeros, tensor_scale)
-        self.device = codes.device
+        self.device, self.index = codes.device, codes.device.index
+        self._need = {}  # workspace bytes by T
         self.c = moe_linear_weights(self.fmt, self.n_out, K, p)
         self.at = ctypes.addressof(self.c)
 
 
 def moe_linear_workspace_bytes(T: int, W: LinearWeights) -> int:
-    return lib().moe_linear_workspace_bytes(T, W.at)
+    need = W._need.get(T)
+    if need is None:
+        need = W._need[T] = lib().moe_linear_workspace_bytes(T, W.at)
+    return need
 
 
 def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] = None,
@@ -750,22 +750,25 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
     """x [T][k_in] bf16 (rows contiguous) times W^T, plus an fp32 bias [n_out] -> y [T][n_out] in `dtype` (or in
     `out`'s type, whose rows may be strided)."""
     T = x.shape[0]
-    dev = x.device
-    if W.device != dev or (bias is not None and bias.device != dev):
-        raise ValueError(f"moe_linear: x is on {dev}, the weights on {W.device}")
-    xs = _rows("moe_linear: x", x, W.k_in)
+    gpu = _gpu(x)
+    if W.index != gpu:
+        raise ValueError(f"moe_linear: x is on GPU {gpu}, the weights on {W.device}")
+    xs = _rows("moe_linear: x", x, T, W.k_in, gpu)
     if bias is not None:
         _dense("moe_linear: bias", bias, torch.float32, (W.n_out,))
+        if bias.device.index != gpu:
+            raise ValueError(f"moe_linear: x is on GPU {gpu}, the bias on {bias.device}")
     if out is None:
-        out = torch.empty((T, W.n_out), dtype=dtype, device=dev)
-    elif out.shape[0] != T:
-        raise ValueError(f"moe_linear: {T} rows of x, {out.shape[0]} of out")
-    ys = _rows("moe_linear: out", out, W.n_out, dev)
-    ws = workspace if workspace is not None else _workspace(moe_linear_workspace_bytes(T, W), dev)
-    with _on(dev) as stream:
-        _check(lib().moe_linear(x.data_ptr(), _act_dtype(x), xs, T, W.at, None if bias is None else bias.data_ptr(),
-                                out.data_ptr(), _dtype("out", out), ys, None if ws is None else ws.data_ptr(),
-                                0 if ws is None else ws.numel(), stream), "moe_linear")
+        out = torch.empty((T, W.n_out), dtype=dtype, device=x.device)
+    ys = _rows("moe_linear: out", out, T, W.n_out, gpu)
+    ws = workspace
+    if ws is None:
+        need = moe_linear_workspace_bytes(T, W)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _enqueue("moe_linear", gpu, x.data_ptr(), _act_dtype(x), xs, T, W.at, None if bias is None else bias.data_ptr(),
+             out.data_ptr(), _dtype("out", out), ys, None if ws is None else ws.data_ptr(),
+             0 if ws is None else ws.numel())
     return out
 
 
