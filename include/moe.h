@@ -471,7 +471,7 @@ moe_status moe_add_rms_norm(const moe_norm *norm, const void *x, moe_dtype x_dty
  *   bias [n_out] fp32, or NULL
  *   y    [T] rows of n_out values (bf16, fp16 or fp32), y_row_stride values apart (>= n_out), aligned to a value
  *   workspace moe_linear_workspace_bytes(T, W) bytes, 16-byte aligned (NULL if that is 0)
- * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^25 bytes or more, or an x row stride of
+ * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^24 bytes or more, or an x row stride of
  * 2^23 values or more), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
 typedef struct {
   moe_w_format fmt;

@@ -787,8 +787,9 @@ moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride
   const moe_status st = check_proj(W->w, W->fmt, 1, W->n_out, W->k_in);
   if (st != MOE_OK) return st;
   const int64_t most = INT64_MAX / 4 / T;
-  // (64 weight rows and 128 rows of x are addressed with 31-bit buffer offsets)
-  if (W->w.w_row_stride >= (int64_t)1 << 25 || W->w.s_row_stride >= (int64_t)1 << 25 || W->w.z_row_stride >= (int64_t)1 << 25 || x_row_stride < W->k_in || x_row_stride >= (int64_t)1 << 23 ||
+  // (128 rows of W and of x are addressed with 31-bit buffer offsets)
+  const int64_t far = (int64_t)1 << 24;
+  if (W->w.w_row_stride >= far || W->w.s_row_stride >= far || W->w.z_row_stride >= far || x_row_stride < W->k_in || x_row_stride >= (int64_t)1 << 23 ||
       y_row_stride < W->n_out || y_row_stride > most)
     return MOE_ERR_SHAPE;
   if (!al16(x) || x_row_stride % 8 != 0 || !al_value(y, y_dtype) || (bias && !al4(bias))) return MOE_ERR_ALIGN;

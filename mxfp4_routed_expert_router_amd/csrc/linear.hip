@@ -84,32 +84,6 @@ __device__ __forceinline__ Blk<FMT> unpack_block(u32x4 codes, uint32_t w, bool i
   }
   return b;
 }
-// A block as loaded from memory, its scale bytes (and the byte of its zero point) not yet converted.
-struct RawBlk {
-  u32x4 q;
-  uint32_t s, z;
-};
-// odd: the block's index is odd (its zero point is the high nibble).  in: it lies inside K.
-template <int FMT>
-__device__ __forceinline__ Blk<FMT> unpack_raw(const RawBlk& r, int odd, bool in) {
-  Blk<FMT> b;
-  b.q = r.q;
-  if constexpr (FMT == MOE_W_MXFP4) {
-    b.s0 = in ? e8m0_to_f32(r.s) : 0.0f;
-    b.s1 = 0.0f;
-  } else {
-    const uint32_t s = in ? r.s : 0u;
-    if constexpr (FMT == MOE_W_INT4_G32) {
-      b.s0 = (float)bitcast<_Float16>((uint16_t)s);
-      b.s1 = -(float)((r.z >> (4 * odd)) & 15u) * b.s0;
-    } else {
-      b.s0 = e4m3_value(s & 255u);
-      b.s1 = e4m3_value(s >> 8);
-    }
-  }
-  return b;
-}
-
 // Four consecutive outputs n .. n+3 of token t from their sums.
 template <int FMT>
 __device__ __forceinline__ void store_out(const LinArgs& a, int t, int n, f32x4 v, float ts) {
@@ -459,13 +433,33 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
 }
 
 // ---- many tokens: tiles of 128 rows of W x 32 MTW tokens, four waves of 64 rows x 16 MTW tokens ----
-// A step is 128 values of K.  Its x (256 bytes per token) goes through a two-stage LDS ring, loaded into registers
-// PD steps ahead; 16-byte piece p of token t lies at piece p ^ (t % 16), so that the 16 tokens of an MFMA operand
-// read distinct banks.  Weights never touch LDS: a lane loads its row's block (16 bytes) in MFMA layout PD steps
-// ahead and decodes it in registers (twice per workgroup, since two waves share a row: 4 conversions per MFMA
-// operand that then serves MTW instructions).  With few tiles the workgroups of a tile share K (splits) and leave
-// fp32 partial sums, which linear_join_kernel adds in order.
-constexpr int kStep = 128;
+// K runs in spans of 256 values, each in four steps of 64.  Weights: the workgroup loads a span of codes (whole
+// 128-byte lines, eight neighbouring lanes per row) and scale bytes into registers one span ahead, and passes them
+// to the other of two LDS buffers a quarter per step; waves read them in MFMA layout and decode in registers.  x:
+// 128 bytes per token and step, loaded XD steps ahead, through a two-stage LDS ring.  (Loading codes and scales
+// straight in MFMA layout, 16 rows x 4 lanes, cost the address unit one cycle per lane: 2048 tokens x 4096 x 7168
+// took 146 us, 118 us so.)  16-byte pieces are exchanged inside a row so that the rows of an MFMA operand read
+// distinct banks.  With few tiles the workgroups of a tile share K (splits) and leave fp32 partial sums, which
+// linear_join_kernel adds in order.
+constexpr int kRowsT = 128;  // rows of a tile
+
+// MFMA operands of two dwords (sixteen codes, half `h` of a 32-value block) and the block's scale word; INT4 also
+// the low operands.  Codes and scale words past K are zero, and so are their weights.
+template <int FMT>
+__device__ __forceinline__ void decode_half(u32x2 c, uint32_t w, int h, bf16x8 (&hi)[2], bf16x8 (&lo)[2]) {
+  Blk<FMT> b;
+  b.q = u32x4{c[0], c[1], 0u, 0u};
+  if constexpr (FMT == MOE_W_MXFP4) {
+    b.s0 = e8m0_to_f32(w);
+  } else if constexpr (FMT == MOE_W_INT4_G32) {
+    b.s0 = (float)bitcast<_Float16>((uint16_t)w);
+    b.s1 = -(float)(w >> 16) * b.s0;
+  } else {
+    b.s0 = e4m3_value((w >> (8 * h)) & 255u);
+  }
+  hi[0] = decode<FMT>(b, 0, lo[0]);
+  hi[1] = decode<FMT>(b, 1, lo[1]);
+}
 
 template <int DT>
 __device__ __forceinline__ void store4(const LinArgs& a, int t, int n, f32x4 v, bool vec) {
@@ -505,59 +499,64 @@ __device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f
     }
 }
 
-template <int FMT, int MTW, int PD>
+template <int FMT, int MTW>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_tiles, int n_tiles, int splits) {
-  constexpr int kTok = 32 * MTW, kStage = kTok * 256;  // tokens, LDS bytes of a stage
-  constexpr int kXL = kStage / 16 / 256;               // 16-byte pieces of x per thread and step
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int kTok = 32 * MTW, kX = kTok * 128, kW = kRowsT * 128, kS = kRowsT * 8;
+  __shared__ __attribute__((aligned(16))) uint8_t xbuf[2][kX];
+  __shared__ __attribute__((aligned(16))) uint8_t wbuf[2][kW];
+  __shared__ uint32_t sbuf[2][kS];  // [row][8]: a block's scale word
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int l16 = lane & 15, q = lane >> 4;
   const int split = blockIdx.x / (t_tiles * n_tiles), tile = blockIdx.x % (t_tiles * n_tiles);
-  const int t0 = (tile % t_tiles) * kTok, nw = (tile / t_tiles) * 128 + (wave >> 1) * 64;
-  const int tw = (wave & 1) * 16 * MTW;  // the wave's first token in the tile
-  // K in turns of PD steps (the last one may pass the end of K)
-  const int blocks = a.K / 32, turns = (a.K + PD * kStep - 1) / (PD * kStep);
-  const int k0 = PD * (int)((int64_t)turns * split / splits), k1 = PD * (int)((int64_t)turns * (split + 1) / splits);
-
+  const int t0 = (tile % t_tiles) * kTok, n0 = (tile / t_tiles) * kRowsT;
+  const int wn = (wave >> 1) * 64, wt = (wave & 1) * 16 * MTW;  // the wave's first row and token in the tile
+  const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
+  const int p0 = (int)((int64_t)spans * split / splits), n = (int)((int64_t)spans * (split + 1) / splits) - p0;
   // As in the streaming kernel, a load's per-lane offset holds the row and is checked (rows past N and tokens past
-  // T read zeros; so does a lane past K), the uniform offset adds the place in K.  No load is conditional: the
+  // T read zeros; so do lanes past K), the uniform offset adds the place in K.  No load is conditional: the
   // registers of loads in flight would be merged, and waited for, at the end of each turn.
   constexpr int kPer = FMT == MOE_W_MXFP4 ? 1 : 2;  // scale bytes per block
-  const int rows = max(0, min(64, a.N - nw)), toks = min(kTok, a.T - t0);
-  const __amdgpu_buffer_rsrc_t wr =
-      make_rsrc(a.w.w + (int64_t)nw * a.w.wr, rows ? (int64_t)(rows - 1) * a.w.wr + a.K / 2 : 0);
+  const int rows = min(kRowsT, a.N - n0), toks = min(kTok, a.T - t0);
+  const __amdgpu_buffer_rsrc_t wr = make_rsrc(a.w.w + (int64_t)n0 * a.w.wr, (int64_t)(rows - 1) * a.w.wr + a.K / 2);
   const __amdgpu_buffer_rsrc_t sr =
-      make_rsrc(a.w.s + (int64_t)nw * a.w.sr, rows ? (int64_t)(rows - 1) * a.w.sr + kPer * blocks : 0);
+      make_rsrc(a.w.s + (int64_t)n0 * a.w.sr, (int64_t)(rows - 1) * a.w.sr + kPer * blocks);
   const __amdgpu_buffer_rsrc_t zr =
-      FMT == MOE_W_INT4_G32
-          ? make_rsrc(a.w.z + (int64_t)nw * a.w.zr, rows ? (int64_t)(rows - 1) * a.w.zr + (blocks + 1) / 2 : 0)
-          : sr;
+      FMT == MOE_W_INT4_G32 ? make_rsrc(a.w.z + (int64_t)n0 * a.w.zr, (int64_t)(rows - 1) * a.w.zr + (blocks + 1) / 2)
+                            : sr;
   const __amdgpu_buffer_rsrc_t xr =
       make_rsrc(a.x + (int64_t)t0 * a.x_stride, ((int64_t)(toks - 1) * a.x_stride + a.K) * 2);
-  const uint32_t woff = (uint32_t)(l16 * a.w.wr) + 16u * q, soff = (uint32_t)(l16 * a.w.sr) + kPer * q;
-  const uint32_t zoff = (uint32_t)(l16 * a.w.zr) + (q >> 1);
-  const uint32_t xoff = (uint32_t)((threadIdx.x >> 4) * a.x_stride) * 2u + 16u * (threadIdx.x & 15);
-  auto load_w = [&](int k, RawBlk (&w)[4]) {
-    const uint32_t out = 4 * k + q < blocks ? 0u : kOutOfRange;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      w[r].q = bld16s(wr, (woff + (uint32_t)(16 * r * a.w.wr)) | out, 64u * k);
-      w[r].s = bld_scale<FMT>(sr, (soff + (uint32_t)(16 * r * a.w.sr)) | out, 4u * kPer * k);
-      w[r].z = 0;
-      if constexpr (FMT == MOE_W_INT4_G32)
-        w[r].z = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(16 * r * a.w.zr)) | out, 2u * k, 0);
-    }
+  const int pr = tid >> 3, pc = tid & 7;  // this thread's rows pr + 32 i and block (piece of x) pc of a row
+  const uint32_t woff = (uint32_t)(pr * a.w.wr) + 16u * pc, soff = (uint32_t)(pr * a.w.sr) + kPer * pc;
+  const uint32_t zoff = (uint32_t)(pr * a.w.zr) + (pc >> 1), xoff = (uint32_t)(pr * a.x_stride) * 2u + 16u * pc;
+  constexpr int XD = 2;  // steps of x in flight (four: the same time, and spills in the INT4 kernel)
+  u32x4 codes[4], x[XD][MTW];  // row group i of the next span; pieces i of the next steps
+  uint32_t sc[4], zp[4];
+  auto load_w = [&](int turn, int i) {
+    const int p = p0 + turn;
+    const uint32_t out = turn < n && 8 * p + pc < blocks ? 0u : kOutOfRange;
+    codes[i] = bld16s(wr, (woff + (uint32_t)(32 * i * a.w.wr)) | out, 128u * p);
+    sc[i] = bld_scale<FMT>(sr, (soff + (uint32_t)(32 * i * a.w.sr)) | out, 8u * kPer * p);
+    if constexpr (FMT == MOE_W_INT4_G32)
+      zp[i] = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(32 * i * a.w.zr)) | out, 4u * p, 0);
   };
-  auto load_x = [&](int k, u32x4 (&x)[kXL]) {
-    const uint32_t out = kStep * k + 8 * (int)(threadIdx.x & 15) < a.K ? 0u : kOutOfRange;
-#pragma unroll
-    for (int i = 0; i < kXL; ++i) x[i] = bld16s(xr, (xoff + (uint32_t)(16 * i * a.x_stride) * 2u) | out, 256u * k);
+  auto put_w = [&](int buf, int i) {
+    const int row = pr + 32 * i;
+    st16(wbuf[buf] + 128 * row + 16 * (pc ^ ((row >> 1) & 7)), codes[i]);
+    sbuf[buf][8 * row + pc] = scale_word<FMT>(sc[i], zp[i], pc & 1);
   };
-  auto put_x = [&](int stage, const u32x4 (&x)[kXL]) {
+  // set: step % XD, given apart so that it is a constant
+  auto load_x = [&](int step, int set) {
+    const int turn = step >> 2, k = kSpan * (p0 + turn) + 64 * (step & 3);
+    const uint32_t out = turn < n && k + 8 * pc < a.K ? 0u : kOutOfRange;
 #pragma unroll
-    for (int i = 0; i < kXL; ++i) {
-      const int f = threadIdx.x + 256 * i, t = f >> 4, c = f & 15;
-      st16(lds + stage * kStage + 256 * t + 16 * (c ^ (t & 15)), x[i]);
+    for (int i = 0; i < MTW; ++i)
+      x[set][i] = bld16s(xr, (xoff + (uint32_t)(32 * i * a.x_stride) * 2u) | out, 2u * k);
+  };
+  auto put_x = [&](int stage, int set) {
+#pragma unroll
+    for (int i = 0; i < MTW; ++i) {
+      const int t = pr + 32 * i;
+      st16(xbuf[stage] + 128 * t + 16 * (pc ^ (t & 7)), x[set][i]);
     }
   };
   f32x4 acc[4][MTW];
@@ -565,52 +564,55 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
   for (int r = 0; r < 4; ++r)
 #pragma unroll
     for (int m = 0; m < MTW; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
-  static_assert(PD % 2 == 0, "the LDS stage of an unrolled step is fixed");
-  RawBlk w[PD][4];
-  u32x4 x[PD][kXL];  // x of step k in set k % PD (counted from k0)
 #pragma unroll
-  for (int d = 0; d < PD; ++d) {
-    load_w(k0 + d, w[d]);
-    load_x(k0 + d, x[d]);
+  for (int i = 0; i < 4; ++i) load_w(0, i);
+#pragma unroll
+  for (int c = 0; c < XD; ++c) load_x(c, c);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    put_w(0, i);
+    load_w(1, i);
   }
-  put_x(0, x[0]);
-  load_x(k0 + PD, x[0]);
+  put_x(0, 0);
+  load_x(XD, 0);
   __syncthreads();
-  for (int kb = k0; kb < k1; kb += PD) {
+  for (int turn = 0; turn < n; ++turn) {
+    const int buf = turn & 1;
 #pragma unroll
-    for (int d = 0; d < PD; ++d) {
-      const int k = kb + d;
-      const int stage = d & 1;
-      const bool in = 4 * k + q < blocks;  // (MXFP4: scale code 0 is not 0)
-      Blk<FMT> b[4];
+    for (int c = 0; c < 4; ++c) {
+      const int stage = c & 1, b = 2 * c + (q >> 1);  // this lane's block of the span
+      bf16x8 xf[MTW][2];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) b[r] = unpack_raw<FMT>(w[d][r], q & 1, in);
+      for (int m = 0; m < MTW; ++m)
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bf16x8 xf[MTW];
+        for (int s = 0; s < 2; ++s)
+          xf[m][s] = bitcast<bf16x8>(ld16(xbuf[stage] + 128 * (wt + 16 * m + l16) + 16 * ((2 * q + s) ^ (l16 & 7))));
 #pragma unroll
-        for (int m = 0; m < MTW; ++m)
-          xf[m] = bitcast<bf16x8>(ld16(lds + stage * kStage + 256 * (tw + 16 * m + l16) + 16 * ((4 * q + s) ^ l16)));
+      for (int r = 0; r < 4; ++r) {
+        const int row = wn + 16 * r + l16;
+        const u32x2 cd =
+            *reinterpret_cast<const u32x2*>(wbuf[buf] + 128 * row + 16 * (b ^ ((l16 >> 1) & 7)) + 8 * (q & 1));
+        bf16x8 hi[2], lo[2];
+        decode_half<FMT>(cd, sbuf[buf][8 * row + b], q & 1, hi, lo);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          bf16x8 lo;
-          const bf16x8 hi = decode<FMT>(b[r], s, lo);
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
           for (int m = 0; m < MTW; ++m) {
-            acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[m], acc[r][m], 0, 0, 0);
+            acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[s], xf[m][s], acc[r][m], 0, 0, 0);
             if constexpr (FMT == MOE_W_INT4_G32)
-              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[m], acc[r][m], 0, 0, 0);
+              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[s], xf[m][s], acc[r][m], 0, 0, 0);
           }
-        }
       }
-      __builtin_amdgcn_sched_barrier(0);  // the waits for the next step's x stay behind the products
-      put_x(stage ^ 1, x[(d + 1) % PD]);
-      load_w(k + PD, w[d]);
-      load_x(k + 1 + PD, x[(d + 1) % PD]);
+      __builtin_amdgcn_sched_barrier(0);  // the waits for the next step's data stay behind the products
+      put_x(stage ^ 1, (c + 1) % XD);
+      put_w(buf ^ 1, c);
+      load_x(4 * turn + c + 1 + XD, (c + 1) % XD);
+      load_w(turn + 2, c);
       __syncthreads();
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  const int tw = wt, nw = n0 + wn;
   // lane: rows 4q + i of row tile r, token l16 of token tile m
   f32x4 bias[4];
 #pragma unroll
@@ -634,20 +636,34 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
   else tile_out<FMT, MTW, MOE_DT_FP16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
 }
 
-// y = the partial sums of the splits in order, with the tensor scale and the bias.
+// y = the partial sums of the splits in order, with the tensor scale and the bias.  All of a thread's loads are
+// issued before the first addition (one after another they took 11 us for 128 tokens x 7168, eight splits).
+constexpr int kMaxSplits = 8;
 template <int FMT>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int n4 = (a.N + 3) / 4;
   if (i >= (int64_t)a.T * n4) return;
   const int t = (int)(i / n4), n = (int)(i % n4) * 4;
-  const float* p = reinterpret_cast<const float*>(a.ws) + (int64_t)t * a.N + n;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < splits; ++s, p += (int64_t)a.T * a.N)
+  const float* p = reinterpret_cast<const float*>(a.ws) + (int64_t)t * a.N + min(n, max(a.N - 4, 0));
+  const int64_t plane = (int64_t)a.T * a.N;
+  const float ts = FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f;
+  if (n + 4 <= a.N) {
+    f32x4 v[kMaxSplits], sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < a.N) v[e] += p[e];
-  store_out<FMT>(a, t, n, v, FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f);
+    for (int s = 0; s < kMaxSplits; ++s) __builtin_memcpy(&v[s], p + min(s, splits - 1) * plane, 16);
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+      if (s < splits) sum += v[s];
+    store_out<FMT>(a, t, n, sum, ts);
+  } else {  // the last columns of a row
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < splits; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < a.N) sum[e] += reinterpret_cast<const float*>(a.ws)[s * plane + (int64_t)t * a.N + n + e];
+    store_out<FMT>(a, t, n, sum, ts);
+  }
 }
 
 // Eight rows per workgroup; eight waves where the rows give at most a workgroup per CU (one token, 1000 x 2080
@@ -677,18 +693,20 @@ void launch_stream_tokens(const LinArgs& a, hipStream_t stream) {
 
 constexpr int kStreamTokens = 64;  // at most this many tokens stream the weights
 
-// Tiles and K shares of the tile kernel: 64-token tiles where 128 would leave half of the tile empty; K shared
-// until there are two workgroups per CU, at least four steps each.
+// Tiles and K shares of the tile kernel.  128-token tiles where they give a workgroup per CU (2048 tokens x 4096 x
+// 7168 MXFP4: 125 us, 156 with 64), 64-token ones below (128 tokens x 2048 x 7168: 17 us, 21 with 128).  K is shared
+// until there are up to two workgroups per CU, at least two spans each, unless the tiles alone come near one per CU
+// (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
 struct TilePlan {
   int mtw, t_tiles, n_tiles, splits;
 };
 TilePlan tile_plan(int T, int N, int K) {
   TilePlan p;
-  p.mtw = (T + 127) / 128 * 128 - T >= 64 ? 2 : 4;
+  p.n_tiles = (N + kRowsT - 1) / kRowsT;
+  p.mtw = (int64_t)((T + 127) / 128) * p.n_tiles >= 256 ? 4 : 2;
   p.t_tiles = (T + 32 * p.mtw - 1) / (32 * p.mtw);
-  p.n_tiles = (N + 127) / 128;
   const int64_t tiles = (int64_t)p.t_tiles * p.n_tiles;
-  const int64_t most = std::min<int64_t>(8, std::max(1, K / (4 * kStep)));
+  const int64_t most = tiles >= 192 ? 1 : std::min<int64_t>(kMaxSplits, std::max(1, K / (2 * kSpan)));
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / tiles));
   return p;
 }
@@ -708,9 +726,9 @@ hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
   const int64_t g = (int64_t)p.t_tiles * p.n_tiles * p.splits;
   if (g > 0x7FFFFF) return hipErrorInvalidConfiguration;  // (more than 2^31 threads)
   if (p.mtw == 2)
-    linear_tile_kernel<FMT, 2, 2><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
+    linear_tile_kernel<FMT, 2><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
   else
-    linear_tile_kernel<FMT, 4, 2><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
+    linear_tile_kernel<FMT, 4><<<dim3((unsigned)g), 256, 0, stream>>>(a, p.t_tiles, p.n_tiles, p.splits);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || p.splits == 1) return err;
   const int64_t n = (int64_t)a.T * ((a.N + 3) / 4);

@@ -122,8 +122,8 @@ def test_linear_refusals(fmt):
     assert L.moe_linear(None, 0, 0, 0, None, None, None, 0, 0, None, 0, None) == OK
     assert L.moe_linear(fake(), 0, 64, 4, None, None, fake(), 2, 32, None, 0, None) == NULL
     assert f(x=None) == NULL and f(y=None) == NULL and f(D(w=None)) == NULL and f(D(scales=None)) == NULL
-    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62), dict(d=D(s_row_stride=1 << 25)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
-                dict(d=D(w_row_stride=16)), dict(d=D(s_row_stride=1)), dict(d=D(w_row_stride=1 << 25))):
+    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62), dict(d=D(s_row_stride=1 << 24)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
+                dict(d=D(w_row_stride=16)), dict(d=D(s_row_stride=1)), dict(d=D(w_row_stride=1 << 24))):
         assert f(**bad) == SHAPE, bad
     assert f(D(k_in=48)) == BLOCK and f(D(w=P + 8)) == BLOCK and f(D(w_row_stride=40)) == BLOCK
     assert f(xdt=1) == DTYPE and f(ydt=3) == DTYPE and f(D(fmt=m.MOE_W_FP16)) == DTYPE and f(D(fmt=9)) == DTYPE
