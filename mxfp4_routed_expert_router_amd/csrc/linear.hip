@@ -41,14 +41,21 @@ __device__ __forceinline__ bf16x8 decode(const Blk<FMT>& r, int s, bf16x8& lo) {
     return bitcast<bf16x8>(u32x4{pack_high(v0[0] * sc, v0[1] * sc), pack_high(v1[0] * sc, v1[1] * sc),
                                  pack_high(v2[0] * sc, v2[1] * sc), pack_high(v3[0] * sc, v3[1] * sc)});
   } else {
+    // a code c as an E4M3 byte is c 2^-9, for every c of four bits
     uint32_t hi[4], l[4];
+    const uint32_t even = r.q[s] & 0x0F0F0F0Fu, odd = (r.q[s] >> 4) & 0x0F0F0F0Fu;
+    const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.0f, false);
+    const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.0f, true);
+    const f32x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.0f, false);
+    const f32x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.0f, true);
+    const float ce[4] = {e0[0], e0[1], e1[0], e1[1]}, co[4] = {o0[0], o0[1], o1[0], o1[1]};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t c = r.q[s] >> (8 * i);
-      const float v0 = __builtin_fmaf((float)(c & 15u), r.s0, r.s1);  // exact: at most 15 bits
-      const float v1 = __builtin_fmaf((float)((c >> 4) & 15u), r.s0, r.s1);
+      const float v0 = __builtin_fmaf(ce[i], r.s0, r.s1);  // exact: at most 15 bits
+      const float v1 = __builtin_fmaf(co[i], r.s0, r.s1);
+      const uint32_t h0 = __float_as_uint(v0) & 0xFFFF0000u, h1 = __float_as_uint(v1) & 0xFFFF0000u;
       hi[i] = pack_high(v0, v1);  // truncated; the rest has at most 7 bits
-      l[i] = pack_high(v0 - __uint_as_float(hi[i] << 16), v1 - __uint_as_float(hi[i] & 0xFFFF0000u));
+      l[i] = pack_high(v0 - __uint_as_float(h0), v1 - __uint_as_float(h1));
     }
     lo = bitcast<bf16x8>(u32x4{l[0], l[1], l[2], l[3]});
     return bitcast<bf16x8>(u32x4{hi[0], hi[1], hi[2], hi[3]});
@@ -432,7 +439,10 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
   }
 }
 
-// ---- many tokens: tiles of 128 rows of W x 32 MTW tokens, four waves of 64 rows x 16 MTW tokens ----
+// ---- many tokens: tiles of 128 rows of W x 32 MTW tokens, shared by four waves ----
+// Two by two waves of 64 rows x 16 MTW tokens, so that two waves decode each weight; INT4, whose decoding takes the
+// vector ALU about as long as its two MFMAs take the matrix core, has four waves of 32 rows x all tokens (WT = 1),
+// which decodes each weight once and reads twice the x from LDS (2048 tokens x 4096 x 7168: 280 -> 201 us).
 // K runs in spans of 256 values, each in four steps of 64.  Weights: the workgroup loads a span of codes (whole
 // 128-byte lines, eight neighbouring lanes per row) and scale bytes into registers one span ahead, and passes them
 // to the other of two LDS buffers a quarter per step; waves read them in MFMA layout and decode in registers.  x:
@@ -483,14 +493,14 @@ __device__ __forceinline__ void store4(const LinArgs& a, int t, int n, f32x4 v, 
 }
 
 // A wave's outputs: rows n + 16 r + i of token t + 16 m from acc[r][m][i].
-template <int FMT, int MTW, int DT>
-__device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f32x4 (&acc)[4][MTW],
-                                         const f32x4 (&bias)[4], float ts, bool vec) {
+template <int FMT, int DT, int RW, int MW>
+__device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f32x4 (&acc)[RW][MW],
+                                         const f32x4 (&bias)[RW], float ts, bool vec) {
 #pragma unroll
-  for (int m = 0; m < MTW; ++m)
+  for (int m = 0; m < MW; ++m)
     if (t + 16 * m < a.T) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < RW; ++r) {
         f32x4 v = acc[r][m];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = FMT == MOE_W_NVFP4 ? __builtin_fmaf(v[e], ts, bias[r][e]) : v[e] + bias[r][e];
@@ -501,6 +511,8 @@ __device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f
 
 template <int FMT, int MTW>
 __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_tiles, int n_tiles, int splits) {
+  constexpr int WT = FMT == MOE_W_INT4_G32 ? 1 : 2;               // waves along the tokens
+  constexpr int RW = 2 * WT, MW = 2 * MTW / WT;                  // a wave's row and token tiles of 16
   constexpr int kTok = 32 * MTW, kX = kTok * 128, kW = kRowsT * 128, kS = kRowsT * 8;
   __shared__ __attribute__((aligned(16))) uint8_t xbuf[2][kX];
   __shared__ __attribute__((aligned(16))) uint8_t wbuf[2][kW];
@@ -509,7 +521,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
   const int l16 = lane & 15, q = lane >> 4;
   const int split = blockIdx.x / (t_tiles * n_tiles), tile = blockIdx.x % (t_tiles * n_tiles);
   const int t0 = (tile % t_tiles) * kTok, n0 = (tile / t_tiles) * kRowsT;
-  const int wn = (wave >> 1) * 64, wt = (wave & 1) * 16 * MTW;  // the wave's first row and token in the tile
+  const int wn = (wave / WT) * 16 * RW, wt = (wave % WT) * 16 * MW;  // the wave's first row and token in the tile
   const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
   const int p0 = (int)((int64_t)spans * split / splits), n = (int)((int64_t)spans * (split + 1) / splits) - p0;
   // As in the streaming kernel, a load's per-lane offset holds the row and is checked (rows past N and tokens past
@@ -559,11 +571,11 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
       st16(xbuf[stage] + 128 * t + 16 * (pc ^ (t & 7)), x[set][i]);
     }
   };
-  f32x4 acc[4][MTW];
+  f32x4 acc[RW][MW];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < RW; ++r)
 #pragma unroll
-    for (int m = 0; m < MTW; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MW; ++m) acc[r][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) load_w(0, i);
 #pragma unroll
@@ -581,14 +593,14 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int stage = c & 1, b = 2 * c + (q >> 1);  // this lane's block of the span
-      bf16x8 xf[MTW][2];
+      bf16x8 xf[MW][2];
 #pragma unroll
-      for (int m = 0; m < MTW; ++m)
+      for (int m = 0; m < MW; ++m)
 #pragma unroll
         for (int s = 0; s < 2; ++s)
           xf[m][s] = bitcast<bf16x8>(ld16(xbuf[stage] + 128 * (wt + 16 * m + l16) + 16 * ((2 * q + s) ^ (l16 & 7))));
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
+      for (int r = 0; r < RW; ++r) {
         const int row = wn + 16 * r + l16;
         const u32x2 cd =
             *reinterpret_cast<const u32x2*>(wbuf[buf] + 128 * row + 16 * (b ^ ((l16 >> 1) & 7)) + 8 * (q & 1));
@@ -597,7 +609,7 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-          for (int m = 0; m < MTW; ++m) {
+          for (int m = 0; m < MW; ++m) {
             acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[s], xf[m][s], acc[r][m], 0, 0, 0);
             if constexpr (FMT == MOE_W_INT4_G32)
               acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[s], xf[m][s], acc[r][m], 0, 0, 0);
@@ -614,9 +626,9 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
   }
   const int tw = wt, nw = n0 + wn;
   // lane: rows 4q + i of row tile r, token l16 of token tile m
-  f32x4 bias[4];
+  f32x4 bias[RW];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int r = 0; r < RW; ++r)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int n = nw + 16 * r + 4 * q + e;
@@ -627,13 +639,13 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
     LinArgs o = a;
     o.y = reinterpret_cast<float*>(a.ws) + (int64_t)split * a.T * a.N;
     o.y_stride = a.N;
-    tile_out<FMT, MTW, MOE_DT_FP32>(o, t0 + tw + l16, nw + 4 * q, acc, bias, ts, a.N % 4 == 0);
+    tile_out<FMT, MOE_DT_FP32>(o, t0 + tw + l16, nw + 4 * q, acc, bias, ts, a.N % 4 == 0);
     return;
   }
   const bool vec = a.y_stride % 4 == 0 && ((uintptr_t)a.y & (a.y_dt == MOE_DT_FP32 ? 15u : 7u)) == 0;
-  if (a.y_dt == MOE_DT_FP32) tile_out<FMT, MTW, MOE_DT_FP32>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
-  else if (a.y_dt == MOE_DT_BF16) tile_out<FMT, MTW, MOE_DT_BF16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
-  else tile_out<FMT, MTW, MOE_DT_FP16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+  if (a.y_dt == MOE_DT_FP32) tile_out<FMT, MOE_DT_FP32>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+  else if (a.y_dt == MOE_DT_BF16) tile_out<FMT, MOE_DT_BF16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
+  else tile_out<FMT, MOE_DT_FP16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
 }
 
 // y = the partial sums of the splits in order, with the tensor scale and the bias.  All of a thread's loads are
