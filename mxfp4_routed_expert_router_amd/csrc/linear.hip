@@ -105,18 +105,18 @@ __device__ __forceinline__ void store_out(const LinArgs& a, int t, int n, f32x4 
 }
 
 // ---- one to four tokens: dot products on the vector ALU ----
-// 8 RG rows per workgroup, whose NW waves share K in spans of 256 values, DP spans in flight each: a lane holds the block lane % 8 of the
-// span of rows lane / 8 + 8 g, so a load instruction takes 8 whole 128-byte lines (nontemporal: used once).  A
-// span of x (512 bytes a token) is loaded as it lies, two tokens per instruction, and passes through LDS of the
-// wave's own to the lanes that need its blocks: loaded in the lanes' order (16 bytes every 64) it took four
-// instructions a token and bound the kernel.  Codes are unpacked to bf16 pairs of small exact integers or E2M1 values, two products per
-// v_dot2_f32_bf16; the block's sum D then takes its scale in fp32:
+// 8 rows per workgroup, whose NW waves share K in spans of 256 values, two spans in flight each (four: the same or
+// slower): a lane holds block lane % 8 of the span of row lane / 8, so a load instruction takes 8 whole 128-byte
+// lines (nontemporal: used once).  A span of x (512 bytes a token) is loaded as it lies, two tokens per instruction,
+// and passes through LDS of the wave's own to the lanes that need its blocks: loaded in the lanes' order (16 bytes
+// every 64) it took four instructions a token and bound the kernel.  Codes are unpacked to bf16 pairs of small exact
+// integers or E2M1 values, two products per v_dot2_f32_bf16; the block's sum D then takes its scale in fp32:
 //   MXFP4, NVFP4  acc += s D       INT4  acc += s (D - z X), X = the sum of the block's x
 // (an unsigned 4-bit code c as an E4M3 byte is c 2^-9 for every c, so INT4 codes unpack by the 8-bit conversion).
+// Bound: one token x 7168 x 7168 MXFP4 reads its 27.3 MB in 7.8 us (3.5 TB/s; of which about 3 us are a launch and
+// the first loads' latency); from three tokens on by the vector ALU (4 tokens of that size 13.7 us).
 constexpr int kSpan = 256;
-constexpr int kDotTokens = 4;
 
-template <int FMT>
 struct DotScale {
   uint32_t s, z;
 };
@@ -139,29 +139,25 @@ __device__ __forceinline__ void unpack_pairs(uint32_t d, bf16x2 (&w)[4]) {
   }
 }
 
-template <int FMT, int TT, int RG, int NW, int DP>
+template <int FMT, int TT, int NW>
 __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
+  constexpr int DP = 2;             // spans in flight
   constexpr int XL = (TT + 1) / 2;  // x loads per span
-  __shared__ float red[NW][RG * 8][TT];
+  __shared__ float red[NW][8][TT];
   __shared__ __attribute__((aligned(16))) uint8_t xlds[NW][XL * 1024];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int lr = lane >> 3, lc = lane & 7;
-  const int n0 = blockIdx.x * 8 * RG;
+  const int n0 = blockIdx.x * 8;
   const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
   const int p0 = (int)((int64_t)spans * wave / NW), p1 = (int)((int64_t)spans * (wave + 1) / NW);
-  const int rows = min(8 * RG, a.N - n0);
+  const int rows = min(8, a.N - n0);
   // rows past N fall past the buffer's range and read zeros
   const __amdgpu_buffer_rsrc_t wr =
       make_rsrc(a.w.w + (int64_t)n0 * a.w.wr, (int64_t)(rows - 1) * a.w.wr + a.K / 2);
   const uint32_t lbase = (uint32_t)(lr * a.w.wr) + 16u * lc;
-  const uint8_t* srow[RG];
-  const uint8_t* zrow[RG];
-#pragma unroll
-  for (int g = 0; g < RG; ++g) {
-    const int64_t n = n0 + min(8 * g + lr, rows - 1);
-    srow[g] = a.w.s + n * a.w.sr;
-    zrow[g] = FMT == MOE_W_INT4_G32 ? a.w.z + n * a.w.zr : nullptr;
-  }
+  const int64_t nr = n0 + min(lr, rows - 1);
+  const uint8_t* const srow = a.w.s + nr * a.w.sr;
+  const uint8_t* const zrow = FMT == MOE_W_INT4_G32 ? a.w.z + nr * a.w.zr : nullptr;
   // this lane's part of x: 16-byte piece lane % 32 of the span of token 2 i + lane / 32 (tokens past the last
   // repeat it; not stored).  Piece i of block b lies at piece i ^ (b / 4) of the block: distinct banks.
   const int xp = lane & 31;
@@ -170,23 +166,19 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
   for (int i = 0; i < XL; ++i) xrow[i] = a.x + (int64_t)min(2 * i + (lane >> 5), a.T - 1) * a.x_stride;
   uint8_t* const xw = xlds[wave] + 512 * (lane >> 5) + 64 * (xp >> 2) + 16 * ((xp & 3) ^ (xp >> 4));
   const uint8_t* const xr = xlds[wave] + 64 * lc;
-  u32x4 codes[DP][RG], x[DP][XL];
-  DotScale<FMT> sc[DP][RG];
-  auto load = [&](int p, u32x4 (&c)[RG], DotScale<FMT> (&s)[RG], u32x4 (&v)[XL]) {
+  u32x4 codes[DP], x[DP][XL];
+  DotScale sc[DP];
+  auto load = [&](int p, u32x4& c, DotScale& s, u32x4 (&v)[XL]) {
     const bool in = p < p1 && 8 * p + lc < blocks;
     const int b = in ? 8 * p + lc : blocks - 1;  // past the wave's share or past K: codes of zero, the rest unused
-#pragma unroll
-    for (int g = 0; g < RG; ++g) c[g] = bld16nt(wr, in ? lbase + (uint32_t)(8 * g * a.w.wr) + 128u * p : kOutOfRange);
-#pragma unroll
-    for (int g = 0; g < RG; ++g) {
-      if constexpr (FMT == MOE_W_MXFP4) {
-        s[g].s = srow[g][b];
-      } else {
-        uint16_t h;
-        __builtin_memcpy(&h, srow[g] + 2 * b, 2);
-        s[g].s = h;
-        if constexpr (FMT == MOE_W_INT4_G32) s[g].z = zrow[g][b >> 1];
-      }
+    c = bld16nt(wr, in ? lbase + 128u * p : kOutOfRange);
+    if constexpr (FMT == MOE_W_MXFP4) {
+      s.s = srow[b];
+    } else {
+      uint16_t h;
+      __builtin_memcpy(&h, srow + 2 * b, 2);
+      s.s = h;
+      if constexpr (FMT == MOE_W_INT4_G32) s.z = zrow[b >> 1];
     }
     const int k = min(kSpan * p + 8 * xp, a.K - 8);
 #pragma unroll
@@ -194,17 +186,15 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
   };
 #pragma unroll
   for (int d = 0; d < DP; ++d) load(p0 + d, codes[d], sc[d], x[d]);
-  float acc[RG][TT];
+  float acc[TT];
 #pragma unroll
-  for (int g = 0; g < RG; ++g)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) acc[g][t] = 0.0f;
+  for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
   auto fence = [] {  // LDS operations of one wave stay in program order
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
-  auto span = [&](int p, const u32x4 (&c)[RG], const DotScale<FMT> (&s)[RG], const u32x4 (&xs)[XL]) {
+  auto span = [&](int p, const u32x4& c, const DotScale& s, const u32x4 (&xs)[XL]) {
     const bool in = p < p1 && 8 * p + lc < blocks;
 #pragma unroll
     for (int i = 0; i < XL; ++i) st16(xw + 1024 * i, xs[i]);
@@ -225,35 +215,32 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
         for (int i = 0; i < 16; ++i) X[t] = __builtin_amdgcn_fdot2_f32_bf16(bitcast<bf16x2>(v[t][i >> 2][i & 3]), one, X[t], false);
       }
     }
+    float D[2][TT];
 #pragma unroll
-    for (int g = 0; g < RG; ++g) {
-      float D[2][TT];
+    for (int t = 0; t < TT; ++t) D[0][t] = D[1][t] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) D[0][t] = D[1][t] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      bf16x2 w[4];
+      unpack_pairs<FMT>(c[i], w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        bf16x2 w[4];
-        unpack_pairs<FMT>(c[g][i], w);
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int t = 0; t < TT; ++t)
+          D[i >> 1][t] = __builtin_amdgcn_fdot2_f32_bf16(w[k], bitcast<bf16x2>(v[t][i][k]), D[i >> 1][t], false);
+    }
 #pragma unroll
-          for (int t = 0; t < TT; ++t)
-            D[i >> 1][t] = __builtin_amdgcn_fdot2_f32_bf16(w[k], bitcast<bf16x2>(v[t][i][k]), D[i >> 1][t], false);
+    for (int t = 0; t < TT; ++t) {
+      float o;
+      if constexpr (FMT == MOE_W_MXFP4) {
+        o = e8m0_to_f32(s.s) * (D[0][t] + D[1][t]);
+      } else if constexpr (FMT == MOE_W_INT4_G32) {
+        const int b = 8 * p + lc;
+        const float z = (float)((s.z >> (4 * (b & 1))) & 15u);
+        o = (float)bitcast<_Float16>((uint16_t)s.s) * __builtin_fmaf(-z, X[t], D[0][t] + D[1][t]);
+      } else {
+        o = __builtin_fmaf(e4m3_value(s.s & 255u), D[0][t], e4m3_value(s.s >> 8) * D[1][t]);
       }
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        float o;
-        if constexpr (FMT == MOE_W_MXFP4) {
-          o = e8m0_to_f32(s[g].s) * (D[0][t] + D[1][t]);
-        } else if constexpr (FMT == MOE_W_INT4_G32) {
-          const int b = 8 * p + lc;
-          const float z = (float)((s[g].z >> (4 * (b & 1))) & 15u);
-          o = (float)bitcast<_Float16>((uint16_t)s[g].s) * __builtin_fmaf(-z, X[t], D[0][t] + D[1][t]);
-        } else {
-          o = __builtin_fmaf(e4m3_value(s[g].s & 255u), D[0][t], e4m3_value(s[g].s >> 8) * D[1][t]);
-        }
-        acc[g][t] += in ? o : 0.0f;
-      }
+      acc[t] += in ? o : 0.0f;
     }
   };
   for (int pb = p0; pb < p1; pb += DP) {
@@ -265,19 +252,18 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
   }
   // over the eight lanes of a row, then over the waves
 #pragma unroll
-  for (int g = 0; g < RG; ++g)
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      float v = acc[g][t];
-      v += __shfl_xor(v, 1, kWave);
-      v += __shfl_xor(v, 2, kWave);
-      v += __shfl_xor(v, 4, kWave);
-      if (lc == 0) red[wave][8 * g + lr][t] = v;
-    }
+  for (int t = 0; t < TT; ++t) {
+    float v = acc[t];
+    v += __shfl_xor(v, 1, kWave);
+    v += __shfl_xor(v, 2, kWave);
+    v += __shfl_xor(v, 4, kWave);
+    if (lc == 0) red[wave][lr][t] = v;
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < RG * 8 * TT; i += 64 * NW) {
-    const int t = i / (RG * 8), r = i % (RG * 8);
-    if (t >= a.T || r >= rows) continue;
+  const int i = threadIdx.x;
+  if (i < 8 * TT) {
+    const int t = i / 8, r = i % 8;
+    if (t >= a.T || r >= rows) return;
     float v = red[0][r][t];
 #pragma unroll
     for (int w = 1; w < NW; ++w) v += red[w][r][t];
@@ -291,16 +277,19 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
 // A span is 256 values of K: 128 bytes of codes per row, so a load instruction (8 rows x 128 bytes) takes whole
 // lines, with the nontemporal hint (a line is used once; the lines of the 16-row x 64-byte shape that the MFMA
 // layout would give read about 13% slower from HBM, and lanes that are neighbours in different rows cost the
-// address unit a cycle each; scale bytes are loaded in the same order for that reason).  A wave keeps DP spans of codes and XP spans of x in flight in
-// registers (one of each serves: eight waves of a CU overlap, and deeper rings measured the same or slower),
-// and turns a span of codes and scales (and half a span of x, 256 bytes a token, four tokens per load) into MFMA
-// layout through LDS of its own.  No load is conditional (registers of loads in flight would be merged, and waited
-// for, at the end of each turn): spans past the wave's share load nothing and add zeros.
-template <int FMT, int RT, int MT, int NW, int DP, int XP>
+// address unit a cycle each; scale bytes are loaded in the same order for that reason).  A wave keeps a span of
+// codes and of x in registers and turns them (x by halves of a span, 256 bytes a token, four tokens per load) into
+// MFMA layout through LDS of its own.  Half a span of x is loaded as soon as the one before it is in LDS (64 tokens,
+// 7168 x 7168 MXFP4: 24.1 us with all loads after the products, 21.2 so), the codes after the span's products
+// (earlier, or two spans ahead: the same or slower).  No load is conditional (registers of loads in flight would be
+// merged, and waited for, at the end of each turn): lanes past K and past the wave's share read zeros.
+// Bound: not by bandwidth (32 tokens, 16384 rows x 4096 NVFP4: 39 MB in 17 us, 2.3 TB/s; 16 tokens, 7168 x 7168
+// MXFP4: 27 MB in 11.2 us).  Reading the weights (5.5 us of the 17), all of x once per workgroup through the L2,
+// both through LDS, and decoding follow one another in each wave, and the registers leave two waves per SIMD.
+template <int FMT, int RT, int MT, int NW>
 __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
   constexpr int kWave = RT * 2048 + RT * 512 + MT * 4096;  // LDS bytes of a wave: its span of codes and scales, its half span of x
   constexpr int kSlots = NW * kWave, kRed = NW * RT * MT * 1024;
-  static_assert(DP % XP == 0, "span d of an unrolled turn uses x set d % XP");
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots > kRed ? kSlots : kRed];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l16 = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
@@ -323,38 +312,34 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
   const uint32_t woff = (uint32_t)(lr * a.w.wr) + 16u * lc;
   const uint32_t soff = (uint32_t)(lr * a.w.sr) + kPer * lc, zoff = (uint32_t)(lr * a.w.zr) + (lc >> 1);
   const uint32_t xoff = (uint32_t)(q * a.x_stride) * 2u + 16u * l16;  // token 4 i + q, piece l16 of a half span
-  u32x4 codes[DP][RT][2], x[XP][2][MT][4];
-  uint32_t sc[DP][RT][2], zp[DP][RT][2];
-  auto load_w = [&](int p, u32x4 (&c)[RT][2], uint32_t (&s)[RT][2], uint32_t (&z)[RT][2]) {
+  u32x4 codes[RT][2], x[2][MT][4];
+  uint32_t sc[RT][2], zp[RT][2];
+  auto load_w = [&](int p) {
     const uint32_t out = p < p1 && 8 * p + lc < blocks ? 0u : kOutOfRange;
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int row = 16 * r + 8 * g;
-        c[r][g] = __builtin_bit_cast(
+        codes[r][g] = __builtin_bit_cast(
             u32x4, __builtin_amdgcn_raw_buffer_load_b128(wr, (woff + (uint32_t)(row * a.w.wr)) | out, 128u * p, 2));
-        s[r][g] = bld_scale<FMT>(sr, (soff + (uint32_t)(row * a.w.sr)) | out, 8u * kPer * p);
-        z[r][g] = 0;
+        sc[r][g] = bld_scale<FMT>(sr, (soff + (uint32_t)(row * a.w.sr)) | out, 8u * kPer * p);
+        zp[r][g] = 0;
         if constexpr (FMT == MOE_W_INT4_G32)
-          z[r][g] = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(row * a.w.zr)) | out, 4u * p, 0);
+          zp[r][g] = __builtin_amdgcn_raw_buffer_load_b8(zr, (zoff + (uint32_t)(row * a.w.zr)) | out, 4u * p, 0);
       }
   };
-  auto load_x = [&](int p, u32x4 (&v)[2][MT][4]) {
+  auto load_x = [&](int p, int j) {
+    const uint32_t out = p < p1 && kSpan * p + 128 * j + 8 * l16 < a.K ? 0u : kOutOfRange;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t out = p < p1 && kSpan * p + 128 * j + 8 * l16 < a.K ? 0u : kOutOfRange;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[j][m][i] = bld16s(xr, (xoff + (uint32_t)((16 * m + 4 * i) * a.x_stride) * 2u) | out, 512u * p + 256u * j);
-    }
+      for (int i = 0; i < 4; ++i)
+        x[j][m][i] = bld16s(xr, (xoff + (uint32_t)((16 * m + 4 * i) * a.x_stride) * 2u) | out, 512u * p + 256u * j);
   };
-#pragma unroll
-  for (int d = 0; d < DP; ++d) load_w(p0 + d, codes[d], sc[d], zp[d]);
-#pragma unroll
-  for (int d = 0; d < XP; ++d) load_x(p0 + d, x[d]);
+  load_w(p0);
+  load_x(p0, 0);
+  load_x(p0, 1);
   f32x4 acc[RT][MT];
 #pragma unroll
   for (int r = 0; r < RT; ++r)
@@ -368,57 +353,55 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
-  for (int pb = p0; pb < p1; pb += DP) {
+  for (int p = p0; p < p1; ++p) {
 #pragma unroll
-    for (int d = 0; d < DP; ++d) {
-      const int p = pb + d;
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+      for (int g = 0; g < 2; ++g) {
+        const int w = 8 * g + lr;
+        st16(slot + 2048 * r + 128 * w + 16 * (lc ^ (w >> 1)), codes[r][g]);
+        sslot[(16 * r + w) * 8 + lc] = scale_word<FMT>(sc[r][g], zp[r][g], lc & 1);
+      }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int w = 8 * g + lr;
-          st16(slot + 2048 * r + 128 * w + 16 * (lc ^ (w >> 1)), codes[d][r][g]);
-          sslot[(16 * r + w) * 8 + lc] = scale_word<FMT>(sc[d][r][g], zp[d][r][g], lc & 1);
-        }
+    for (int j = 0; j < 2; ++j) {
+      const bool in = 8 * p + 4 * j + q < blocks;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bool in = p < p1 && 8 * p + 4 * j + q < blocks;
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          st16(xslot + 4096 * m + 256 * (4 * i + q) + 16 * (l16 ^ (4 * i + q)), x[j][m][i]);
+      load_x(p + 1, j);
+      __builtin_amdgcn_sched_barrier(0);
+      fence();
+      Blk<FMT> b[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        b[r] = unpack_block<FMT>(ld16(slot + 2048 * r + 128 * l16 + 16 * ((4 * j + q) ^ (l16 >> 1))),
+                                 sslot[(16 * r + l16) * 8 + 4 * j + q], in);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        bf16x8 xf[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            st16(xslot + 4096 * m + 256 * (4 * i + q) + 16 * (l16 ^ (4 * i + q)), x[d % XP][j][m][i]);
-        fence();
-        Blk<FMT> b[RT];
+          xf[m] = bitcast<bf16x8>(ld16(xslot + 4096 * m + 256 * l16 + 16 * ((4 * q + k) ^ l16)));
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          b[r] = unpack_block<FMT>(ld16(slot + 2048 * r + 128 * l16 + 16 * ((4 * j + q) ^ (l16 >> 1))),
-                                   sslot[(16 * r + l16) * 8 + 4 * j + q], in);
-        }
+          bf16x8 lo;
+          const bf16x8 hi = decode<FMT>(b[r], k, lo);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          bf16x8 xf[MT];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-            xf[m] = bitcast<bf16x8>(ld16(xslot + 4096 * m + 256 * l16 + 16 * ((4 * q + k) ^ l16)));
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            bf16x8 lo;
-            const bf16x8 hi = decode<FMT>(b[r], k, lo);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[m], acc[r][m], 0, 0, 0);
-              if constexpr (FMT == MOE_W_INT4_G32)
-                acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[m], acc[r][m], 0, 0, 0);
-            }
+          for (int m = 0; m < MT; ++m) {
+            acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, xf[m], acc[r][m], 0, 0, 0);
+            if constexpr (FMT == MOE_W_INT4_G32)
+              acc[r][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, xf[m], acc[r][m], 0, 0, 0);
           }
         }
-        fence();
+        if (k == 1) __builtin_amdgcn_sched_barrier(0);  // (or the reads of all four k come first, and spill)
       }
-      load_w(p + DP, codes[d], sc[d], zp[d]);
-      load_x(p + XP, x[d % XP]);
-      __builtin_amdgcn_sched_barrier(0);  // (a later span's waits stay behind this one's loads)
+      fence();
     }
+    load_w(p + 1);
+    __builtin_amdgcn_sched_barrier(0);  // (the next span's waits stay behind its loads)
   }
   // the waves' sums: [wave][r][m][lane] as four rows of one token
   __syncthreads();
@@ -680,12 +663,12 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits)
 
 // Eight rows per workgroup; eight waves where the rows give at most a workgroup per CU (one token, 1000 x 2080
 // INT4 3.2 against 3.3 us with four waves, 512 x 7168 NVFP4 4.2 against 5.5), four beyond (7168 x 7168 MXFP4 7.9
-// against 9.2).  Two spans in flight: four measured the same or slower.
+// against 9.2).
 template <int FMT, int TT>
 void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
   const dim3 g((unsigned)((a.N + 7) / 8));
-  if (a.N <= 2048) linear_dot_kernel<FMT, TT, 1, 8, 2><<<g, 512, 0, stream>>>(a);
-  else linear_dot_kernel<FMT, TT, 1, 4, 2><<<g, 256, 0, stream>>>(a);
+  if (a.N <= 2048) linear_dot_kernel<FMT, TT, 8><<<g, 512, 0, stream>>>(a);
+  else linear_dot_kernel<FMT, TT, 4><<<g, 256, 0, stream>>>(a);
 }
 
 // Rows per workgroup: every workgroup reads all of x, so as many as leave about 200 workgroups (one per CU).  16
@@ -694,7 +677,7 @@ void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
 template <int FMT, int MT, int RT>
 void launch_stream_rows(const LinArgs& a, hipStream_t stream) {
   constexpr int NW = MT == 4 && RT > 1 ? 4 : 8;
-  linear_stream_kernel<FMT, RT, MT, NW, 1, 1><<<dim3((unsigned)((a.N + 16 * RT - 1) / (16 * RT))), 64 * NW, 0, stream>>>(a);
+  linear_stream_kernel<FMT, RT, MT, NW><<<dim3((unsigned)((a.N + 16 * RT - 1) / (16 * RT))), 64 * NW, 0, stream>>>(a);
 }
 template <int FMT, int MT>
 void launch_stream_tokens(const LinArgs& a, hipStream_t stream) {
@@ -703,12 +686,20 @@ void launch_stream_tokens(const LinArgs& a, hipStream_t stream) {
   else launch_stream_rows<FMT, MT, 1>(a, stream);
 }
 
-constexpr int kStreamTokens = 64;  // at most this many tokens stream the weights
+// Up to 32 tokens stream the weights, and up to 64 while a wave's share of K is short: tiles share K over workgroups,
+// 64 tokens x 2048 rows x 4096 MXFP4 streamed 12.2 us, 14.0 as tiles; x 5120 14.7 and 14.1; x 7168 18.4 and 15.2;
+// 48 x 2048 x 16384 31.6 and 23.1.  From 6400 rows on (32 rows a workgroup) 7168 x 7168 20.7 and 22.4, 7168 x 16384
+// 40.6 and 35.6.
+bool streams(int T, int N, int K) { return T <= 32 || (T <= 64 && K <= (N < 32 * 200 ? 5120 : 8192)); }
+// Three and four tokens: dot products up to this many rows, where the streaming kernel has fewer than 200 workgroups
+// (4 tokens, 2048 x 7168 MXFP4: 6.1 us, streamed 7.5; 4096 x 4096: 5.9 and 5.6; 7168 x 7168: 13.7 and 10.2).  Two
+// tokens are faster by dot products at every size (7168 x 7168 MXFP4 9.1 us and 9.8, INT4 13.0 and 17.3).
+constexpr int kDotRows = 16 * 200;
 
 // Tiles and K shares of the tile kernel.  128-token tiles where they give a workgroup per CU (2048 tokens x 4096 x
 // 7168 MXFP4: 125 us, 156 with 64), 64-token ones below (128 tokens x 2048 x 7168: 17 us, 21 with 128).  K is shared
-// until there are up to two workgroups per CU, at least two spans each, unless the tiles alone come near one per CU
-// (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
+// until there are up to two workgroups per CU, at least a span each (200 tokens x 230 x 1632 INT4: 15.7 us, 17.9
+// with two), unless the tiles alone come near one per CU (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
 struct TilePlan {
   int mtw, t_tiles, n_tiles, splits;
 };
@@ -718,17 +709,17 @@ TilePlan tile_plan(int T, int N, int K) {
   p.mtw = (int64_t)((T + 127) / 128) * p.n_tiles >= 256 ? 4 : 2;
   p.t_tiles = (T + 32 * p.mtw - 1) / (32 * p.mtw);
   const int64_t tiles = (int64_t)p.t_tiles * p.n_tiles;
-  const int64_t most = tiles >= 192 ? 1 : std::min<int64_t>(kMaxSplits, std::max(1, K / (2 * kSpan)));
+  const int64_t most = tiles >= 192 ? 1 : std::min<int64_t>(kMaxSplits, std::max(1, K / kSpan));
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / tiles));
   return p;
 }
 
 template <int FMT>
 hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
-  if (a.T <= kStreamTokens) {
+  if (streams(a.T, a.N, a.K)) {
     if (a.T == 1) launch_dot_tokens<FMT, 1>(a, stream);
     else if (a.T == 2) launch_dot_tokens<FMT, 2>(a, stream);
-    else if (a.T <= kDotTokens) launch_dot_tokens<FMT, 4>(a, stream);
+    else if (a.T <= 4 && a.N <= kDotRows) launch_dot_tokens<FMT, 4>(a, stream);
     else if (a.T <= 16) launch_stream_tokens<FMT, 1>(a, stream);
     else if (a.T <= 32) launch_stream_tokens<FMT, 2>(a, stream);
     else launch_stream_tokens<FMT, 4>(a, stream);
@@ -751,7 +742,7 @@ hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t linear_workspace_bytes(int T, int N, int K) {
-  if (T <= kStreamTokens) return 0;
+  if (streams(T, N, K)) return 0;
   const TilePlan p = tile_plan(T, N, K);
   return p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)T * (size_t)N : 0;
 }

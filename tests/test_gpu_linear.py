@@ -105,6 +105,13 @@ def test_many_rows(fmt, T, N):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,N,K", [(4, 3200, 96), (4, 3201, 96), (33, 70, 5120), (33, 70, 5152), (64, 130, 8192),
+                                   (64, 6400, 5152), (50, 6420, 8192), (40, 6403, 8224), (32, 40, 9216)])
+def test_where_kernels_meet(fmt, T, N, K):
+    check(T, N, K, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T", [1, 3, 12, 30, 60, 150])
 def test_scales_at_any_address(fmt, T):
     """Scale and zero-point rows at odd addresses, an odd number of bytes apart."""
