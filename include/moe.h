@@ -34,7 +34,7 @@
  *  - Validation happens before anything is enqueued; on any error nothing is launched and the
  *    status says why.  T == 0 returns MOE_OK without touching any pointer.
  *  - Inputs are read-only; outputs are overwritten (never accumulated into); buffers must not
- *    alias each other.  Calls that share no output buffer may run concurrently on different
+ *    alias each other (but moe_add_rms_norm's residual_out may be its residual).  Calls that share no output buffer may run concurrently on different
  *    streams.
  *  - Results are deterministic: the same inputs give bit-identical outputs on every run (no
  *    floating-point atomics anywhere).
@@ -193,7 +193,7 @@ typedef struct {
  *   ids     [T][top_k+n_shared] int32 out;  weights [T][top_k+n_shared] fp32 out
  *   scores  [T][E] fp32 out (s; 0 for an expert whose logit is not finite), or NULL
  * One launch, no workspace.
- * Errors: NULL, SHAPE (T<0, E<1, E>MOE_MAX_EXPERTS, n_shared<0, row_stride<E, n_groups outside
+ * Errors: NULL, SHAPE (T<0, T>2^25, E<1, E>MOE_MAX_EXPERTS, n_shared<0, row_stride<E, n_groups outside
  * [1, MOE_MAX_GROUPS] or not a divisor of E, topk_groups outside [1, n_groups], a routed_scale or
  * shared_weight that is not finite), TOPK (top_k < 1 or beyond topk_groups * E/n_groups, or
  * top_k+n_shared > MOE_MAX_SLOTS_PER_TOKEN), DTYPE, ALIGN, HIP. */
@@ -444,8 +444,8 @@ moe_status moe_expert_ffn_mx_codes(const uint8_t *x_codes, const uint8_t *x_scal
  * moe_linear's fp32 output, y is what moe_route, moe_linear and moe_expert_ffn read.
  *   x, residual, residual_out  [T] rows of `hidden` values, *_row_stride values apart (>= hidden), aligned to a
  *       value.  residual may be NULL (then residual_out must be too); residual_out may be NULL, and may be
- *       residual itself (same pointer and stride: the sum replaces it in place; any other overlap is an error
- *       that is not checked)
+ *       residual itself (same pointer and stride: the sum replaces it in place; another stride there is a SHAPE
+ *       error, any other overlap an error that is not checked)
  *   y       [T][hidden], aligned to a value, or NULL
  *   codes   [T] packed rows (moe_mx_row_bytes), 16-byte aligned; scales [T][hidden/32]; fmt 0: both NULL
  * Rows of 8 to 32768 values take the fast kernels.
@@ -471,8 +471,8 @@ moe_status moe_add_rms_norm(const moe_norm *norm, const void *x, moe_dtype x_dty
  *   bias [n_out] fp32, or NULL
  *   y    [T] rows of n_out values (bf16, fp16 or fp32), y_row_stride values apart (>= n_out), aligned to a value
  *   workspace moe_linear_workspace_bytes(T, W) bytes, 16-byte aligned (NULL if that is 0)
- * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^24 bytes or more, or an x row stride of
- * 2^23 values or more), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
+ * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^24 bytes or more, an x row stride of
+ * 2^23 values or more, or n_out > 2^26), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
 typedef struct {
   moe_w_format fmt;
   int n_out, k_in;

@@ -533,7 +533,7 @@ def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: Ex
     dev = x_codes.device
     f = _mx_fmt(fmt)
     _dense("moe_expert_ffn_mx_codes: x_codes", x_codes, torch.uint8, (T, moe_mx_row_bytes(f, W.hidden)))
-    _dense("moe_expert_ffn_mx_codes: x_scales", x_scales, torch.uint8, (T, W.hidden // 32))
+    _dense("moe_expert_ffn_mx_codes: x_scales", x_scales, torch.uint8, (T, W.hidden // 32), dev.index)
     y = out if out is not None else torch.empty((T * k_total, W.hidden), dtype=torch.float32, device=dev)
     ws = workspace if workspace is not None else _workspace(moe_expert_ffn_mx_workspace_bytes(T, k_total, W, f), dev)
     _check(lib().moe_expert_ffn_mx_codes(_ptr(x_codes), _ptr(x_scales), T, k_total, ctypes.byref(W.c), f,
@@ -545,10 +545,13 @@ def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: Ex
 # ----------------------------------------------------------------------------------------------------
 # In front of the layer.  These calls take few microseconds of GPU time at small T: descriptions are built once, a
 # call checks what its pointers cannot tell and passes plain integers.
-def _dense(what: str, t: torch.Tensor, dtype, shape) -> None:
+def _dense(what: str, t: torch.Tensor, dtype, shape, index: Optional[int] = -1) -> None:
+    """Contiguous, of this type and shape, and on GPU `index` (-1: anywhere)."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
+    if index != -1 and t.device.index != index:
+        raise ValueError(f"{what} must be on GPU {index}, got {t.device}")
 
 
 def _rows(what: str, t: torch.Tensor, T: int, width: int, index: Optional[int]) -> int:
@@ -557,6 +560,11 @@ def _rows(what: str, t: torch.Tensor, T: int, width: int, index: Optional[int]) 
         raise ValueError(f"{what} must be [{T}][{width}] with contiguous rows on GPU {index}, got {tuple(t.shape)} on "
                          f"{t.device}")
     return t.stride(0) if T > 1 else width
+
+
+def _on_gpu(what: str, ws: torch.Tensor, index: int) -> None:
+    if ws.device.index != index or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"{what} must be contiguous uint8 on GPU {index}, got {ws.dtype} on {ws.device}")
 
 
 def _dtype(what: str, t: torch.Tensor) -> int:
@@ -613,10 +621,10 @@ def _route_out(what: str, rule: RouteRule, T: int, E: int, dev, want_scores: boo
                 torch.empty((T, kt), dtype=torch.float32, device=dev),
                 torch.empty((T, E), dtype=torch.float32, device=dev) if want_scores else None)
     ids, w, scores = out
-    _dense(f"{what}: ids", ids, torch.int32, (T, kt))
-    _dense(f"{what}: weights", w, torch.float32, (T, kt))
+    _dense(f"{what}: ids", ids, torch.int32, (T, kt), dev.index)
+    _dense(f"{what}: weights", w, torch.float32, (T, kt), dev.index)
     if scores is not None:
-        _dense(f"{what}: scores", scores, torch.float32, (T, E))
+        _dense(f"{what}: scores", scores, torch.float32, (T, E), dev.index)
     return out
 
 
@@ -640,9 +648,13 @@ def moe_route_grouped(x: torch.Tensor, w_router: torch.Tensor, rule: RouteRule, 
     dev = x.device
     gpu = _gpu(x)
     _dense("moe_route_grouped: x", x, x.dtype, (T, H))
-    _dense("moe_route_grouped: w_router", w_router, torch.float32, (E, H))
+    _dense("moe_route_grouped: w_router", w_router, torch.float32, (E, H), gpu)
     ids, w, scores = _route_out("moe_route_grouped", rule, T, E, dev, want_scores, out)
-    ws = workspace if workspace is not None else _workspace(moe_route_workspace_bytes(T, H, E), dev)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(moe_route_workspace_bytes(T, H, E), dev)
+    else:
+        _on_gpu("moe_route_grouped: workspace", ws, gpu)
     _enqueue("moe_route_grouped", gpu, x.data_ptr(), _act_dtype(x), T, H, w_router.data_ptr(), E, rule.at,
              ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr(),
              None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel())
@@ -689,12 +701,13 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
     else:
         y, ro, codes, scales = out
         if y is not None:
-            _dense("moe_add_rms_norm: y", y, y.dtype, (T, H))
+            _dense("moe_add_rms_norm: y", y, y.dtype, (T, H), gpu)
         if f:
             if codes is None or scales is None:
                 raise ValueError("moe_add_rms_norm: mx needs codes and scales")
-            _dense("moe_add_rms_norm: codes", codes, torch.uint8, (T, H if f == MOE_MX_FP8_E4M3 else moe_mx_row_bytes(f, H)))
-            _dense("moe_add_rms_norm: scales", scales, torch.uint8, (T, H // 32))
+            _dense("moe_add_rms_norm: codes", codes, torch.uint8,
+                   (T, H if f == MOE_MX_FP8_E4M3 else moe_mx_row_bytes(f, H)), gpu)
+            _dense("moe_add_rms_norm: scales", scales, torch.uint8, (T, H // 32), gpu)
         if ro is not None and (residual is None or ro.dtype is not residual.dtype):
             raise ValueError("moe_add_rms_norm: residual_out needs a residual of its type")
     if ro is not None:
@@ -755,9 +768,7 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
         raise ValueError(f"moe_linear: x is on GPU {gpu}, the weights on {W.device}")
     xs = _rows("moe_linear: x", x, T, W.k_in, gpu)
     if bias is not None:
-        _dense("moe_linear: bias", bias, torch.float32, (W.n_out,))
-        if bias.device.index != gpu:
-            raise ValueError(f"moe_linear: x is on GPU {gpu}, the bias on {bias.device}")
+        _dense("moe_linear: bias", bias, torch.float32, (W.n_out,), gpu)
     if out is None:
         out = torch.empty((T, W.n_out), dtype=dtype, device=x.device)
     ys = _rows("moe_linear: out", out, T, W.n_out, gpu)
@@ -766,6 +777,8 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
         need = moe_linear_workspace_bytes(T, W)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    else:
+        _on_gpu("moe_linear: workspace", ws, gpu)
     _enqueue("moe_linear", gpu, x.data_ptr(), _act_dtype(x), xs, T, W.at, None if bias is None else bias.data_ptr(),
              out.data_ptr(), _dtype("out", out), ys, None if ws is None else ws.data_ptr(),
              0 if ws is None else ws.numel())
@@ -836,7 +849,11 @@ class MoEBlock:
     without W_o), the residual addition and norm, routing by a rule, bucketing, the expert FFN and the combine.
     With mx ("fp8", "fp6", "fp4") the norm writes the MX codes that the expert FFN reads.
 
-    forward(attn, residual) -> (y fp32 [T][H], residual_out): the next block's norm adds y to residual_out."""
+    forward(attn, residual) -> (y fp32 [T][H], residual_out): the next block's norm adds y to residual_out.
+
+    Whether the rule's selection_bias can leave slots empty (a value of -inf) is read when the block is built: a
+    bias that masks experts only later needs a new block.  Passes of one block share its buffers, so they run one
+    after another on one stream."""
 
     def __init__(self, W: ExpertWeights, T: int, rule: RouteRule, w_router: torch.Tensor, norm: RmsNorm,
                  W_o: Optional[LinearWeights] = None, mx=None):

@@ -685,7 +685,7 @@ moe_status check_rule(const moe_route_rule* r, int T, int E) {
   if (r->top_k < 1 || r->top_k > r->topk_groups * (E / r->n_groups) ||
       (int64_t)r->top_k + r->n_shared > MOE_MAX_SLOTS_PER_TOKEN)
     return MOE_ERR_TOPK;
-  if ((int64_t)T * (r->top_k + r->n_shared) > INT_MAX || (int64_t)T * E > INT_MAX) return MOE_ERR_SHAPE;
+  if ((int64_t)T * (r->top_k + r->n_shared) > INT_MAX || (int64_t)T * E > INT_MAX || T > 1 << 25) return MOE_ERR_SHAPE;
   if (r->selection_bias && !al4(r->selection_bias)) return MOE_ERR_ALIGN;
   return MOE_OK;
 }
@@ -741,7 +741,8 @@ moe_status moe_add_rms_norm(const moe_norm* norm, const void* x, moe_dtype x_dty
   if (fmt != 0 && H % 32 != 0) return MOE_ERR_BLOCK;
   const int64_t most = INT64_MAX / 4 / T;
   if (x_row_stride < H || x_row_stride > most || (residual && (residual_row_stride < H || residual_row_stride > most)) ||
-      (residual_out && (residual_out_row_stride < H || residual_out_row_stride > most)))
+      (residual_out && (residual_out_row_stride < H || residual_out_row_stride > most)) ||
+      (residual_out && residual_out == residual && residual_out_row_stride != residual_row_stride && T > 1))
     return MOE_ERR_SHAPE;
   if (!al_value(x, x_dtype) || !al_value(norm->weight, norm->weight_dtype) ||
       (residual && !al_value(residual, residual_dtype)) || (residual_out && !al_value(residual_out, residual_dtype)) ||
@@ -789,8 +790,8 @@ moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride
   const int64_t most = INT64_MAX / 4 / T;
   // (128 rows of W and of x are addressed with 31-bit buffer offsets)
   const int64_t far = (int64_t)1 << 24;
-  if (W->w.w_row_stride >= far || W->w.s_row_stride >= far || W->w.z_row_stride >= far || x_row_stride < W->k_in || x_row_stride >= (int64_t)1 << 23 ||
-      y_row_stride < W->n_out || y_row_stride > most)
+  if (W->w.w_row_stride >= far || W->w.s_row_stride >= far || W->w.z_row_stride >= far || x_row_stride < W->k_in ||
+      x_row_stride >= far / 2 || y_row_stride < W->n_out || y_row_stride > most || W->n_out > 1 << 26)
     return MOE_ERR_SHAPE;
   if (!al16(x) || x_row_stride % 8 != 0 || !al_value(y, y_dtype) || (bias && !al4(bias))) return MOE_ERR_ALIGN;
   const size_t need = moe_linear_workspace_bytes(T, W);

@@ -6,6 +6,8 @@
 //   codes, scales = MX blocks of the fp32 y (not of the rounded one: one rounding, not two)
 // It reads x and residual and writes residual_out, y and the codes once each, so the bytes bound it; the row
 // stays in registers between the sum and the outputs.
+#include <algorithm>
+
 #include "launch.hpp"
 #include "mx.hpp"
 #include "values.hpp"
@@ -184,6 +186,27 @@ void launch_norm_x(const NormArgs& a, int threads, int nv, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
+  constexpr int kMostRows = 1 << 20;  // of a launch: fewer than 2^32 threads
+  if (a.T > kMostRows) {
+    for (int64_t t = 0; t < a.T; t += kMostRows) {
+      const auto row = [t](auto* p, int64_t values, int dt) {
+        return p ? (decltype(p))((uintptr_t)p + t * values * (dt == MOE_DT_FP32 ? 4 : 2)) : p;
+      };
+      NormArgs b = a;
+      b.x = row(a.x, a.x_stride, a.x_dt);
+      b.residual = row(a.residual, a.r_stride, a.r_dt);
+      b.residual_out = row(a.residual_out, a.ro_stride, a.r_dt);
+      b.y = row(a.y, a.H, a.y_dt);
+      if (a.mx) {
+        b.codes = a.codes + t * a.code_row;
+        b.scales = a.scales + t * (a.H / 32);
+      }
+      b.T = (int)std::min<int64_t>(kMostRows, a.T - t);
+      const hipError_t err = launch_norm(b, stream);
+      if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
+  }
   if (a.H < 8 || a.H > 8 * 1024 * 4) {
     norm_any_kernel<<<dim3((unsigned)a.T), 256, 0, stream>>>(a);
     return hipGetLastError();

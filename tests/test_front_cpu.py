@@ -41,7 +41,7 @@ def test_select_refusals():
     for bad in (dict(T=-1), dict(E=0), dict(E=1025, stride=1025), dict(n_shared=-1), dict(stride=63), dict(n_groups=0),
                 dict(n_groups=65, E=65, stride=65), dict(n_groups=5), dict(n_groups=8, topk_groups=0),
                 dict(n_groups=8, topk_groups=9), dict(routed_scale=float("nan")), dict(shared_weight=float("inf")),
-                dict(stride=1 << 62)):
+                dict(stride=1 << 62), dict(T=(1 << 25) + 1, E=8, stride=8)):
         assert s(**bad) == SHAPE, bad
     for bad in (dict(top_k=0), dict(top_k=65), dict(n_groups=8, topk_groups=2, top_k=17), dict(top_k=60, n_shared=200),
                 dict(n_shared=2 ** 31 - 1)):
@@ -84,7 +84,7 @@ def test_norm_refusals():
                 dict(mx, codes=None), dict(mx, scales=None), dict(codes=fake(2048)), dict(scales=fake(2048))):
         assert n(**bad) == NULL, bad
     for bad in (dict(T=-1), dict(H=0), dict(xs=63), dict(rs=63), dict(ros=0), dict(eps=-1.0), dict(eps=float("nan")),
-                dict(eps=float("inf")), dict(xs=1 << 62)):
+                dict(eps=float("inf")), dict(xs=1 << 62), dict(ro=fake(256), ros=72)):
         assert n(**bad) == SHAPE, bad
     assert n(**dict(mx, H=48, xs=48, rs=48, ros=48)) == BLOCK
     for bad in (dict(xdt=3), dict(rdt=3), dict(ydt=-1), dict(wdt=7), dict(mx, fmt=4), dict(mx, fmt=-1)):
@@ -122,7 +122,9 @@ def test_linear_refusals(fmt):
     assert L.moe_linear(None, 0, 0, 0, None, None, None, 0, 0, None, 0, None) == OK
     assert L.moe_linear(fake(), 0, 64, 4, None, None, fake(), 2, 32, None, 0, None) == NULL
     assert f(x=None) == NULL and f(y=None) == NULL and f(D(w=None)) == NULL and f(D(scales=None)) == NULL
-    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62), dict(d=D(s_row_stride=1 << 24)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
+    for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62),
+                dict(d=D(s_row_stride=1 << 24)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
+                dict(d=D(n_out=(1 << 26) + 1), ys=1 << 27),
                 dict(d=D(w_row_stride=16)), dict(d=D(s_row_stride=1)), dict(d=D(w_row_stride=1 << 24))):
         assert f(**bad) == SHAPE, bad
     assert f(D(k_in=48)) == BLOCK and f(D(w=P + 8)) == BLOCK and f(D(w_row_stride=40)) == BLOCK
