@@ -768,6 +768,7 @@ moe_status moe_add_rms_norm(const moe_norm* norm, const void* x, moe_dtype x_dty
   a.H = H;
   a.mx = fmt;
   a.eps = norm->eps;
+  a.inv_h = 1.0 / H;
   return hip_status(moe::launch_norm(a, (hipStream_t)stream));
 }
 

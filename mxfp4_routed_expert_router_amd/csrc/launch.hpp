@@ -147,6 +147,7 @@ struct NormArgs {
   int x_dt, r_dt, w_dt, y_dt;                       // moe_dtype
   int T, H, mx;                                     // mx: moe_mx_format, 0 for none
   float eps;
+  double inv_h;  // 1 / H
 };
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 

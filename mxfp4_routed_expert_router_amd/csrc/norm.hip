@@ -1,7 +1,7 @@
 // Residual addition and root-mean-square norm, with an optional MX output (8-, 6- or 4-bit codes with one E8M0
 // scale per 32 values, the layout the MX expert FFN reads).  Per row of H values:
 //   s = x + residual                      (fp32; residual_out = s rounded to the residual's type)
-//   r = 1 / sqrt(sum(s^2) / H + eps)      (fp32 sum: per-thread partial sums, then a fixed tree)
+//   r = 1 / sqrt(sum(s^2) / H + eps)      (fp32 sums of a thread and of a wave; from there in 64 bits, rounded once)
 //   y = s * r * weight                    (fp32; rounded once to y's type)
 //   codes, scales = MX blocks of the fp32 y (not of the rounded one: one rounding, not two)
 // It reads x and residual and writes residual_out, y and the codes once each, so the bytes bound it; the row
@@ -16,17 +16,24 @@ namespace moe {
 
 namespace {
 
-// Sum of v over the workgroup, the same value in every thread (fixed order: waves in wave order).
-// red: one float per wave.
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// 1 / sqrt(sum / H + eps) of the workgroup's v, the same value in every thread (fixed order: a wave's lanes by a
+// tree, the waves in wave order).  red: one float per wave.  Joining the waves and the root in 64 bits leave about
+// half an fp32 rounding in r, which every value of the row shares, and take less time than fp32's exact division
+// and square root: the reciprocal root instruction (2^-24 or better) and one Newton step.
+__device__ __forceinline__ float row_scale(const NormArgs& a, float v, float* red) {
   const int wave = threadIdx.x >> 6, n = (blockDim.x + 63) >> 6;
   v = wave_sum_dpp(v);
-  if (n == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[wave] = v;
-  __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < n; ++w) s += red[w];
-  return s;
+  double s = (double)v;
+  if (n > 1) {
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < n; ++w) s += (double)red[w];
+  }
+  const double m = __builtin_fma(s, a.inv_h, (double)a.eps);
+  const double r = __builtin_amdgcn_rsq(m);
+  const double e = __builtin_fma(-m * r, r, 1.0);
+  return (float)(m > 0.0 && m < (double)INFINITY ? __builtin_fma(0.5 * r, e, r) : r);  // (0 and infinity have no step)
 }
 
 // Codes and scale of a 32-value block held by four consecutive lanes, eight values each (element i of the
@@ -100,7 +107,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
     for (int j = 0; j < 8; ++j) p = at[v] + j >= i ? __builtin_fmaf(s[v][j], s[v][j], p) : p;
     sum += i < H ? p : 0.0f;
   }
-  const float rstd = 1.0f / sqrtf(block_sum(sum, red) / (float)H + a.eps);
+  const float rstd = row_scale(a, sum, red);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int i = 8 * (v * (int)blockDim.x + (int)threadIdx.x);
@@ -151,7 +158,7 @@ __global__ __launch_bounds__(256) void norm_any_kernel(NormArgs a) {
     if (a.residual) s += ld_value(a.residual, a.r_dt, t * a.r_stride + i);
     sum = __builtin_fmaf(s, s, sum);
   }
-  const float rstd = 1.0f / sqrtf(block_sum(sum, red) / (float)H + a.eps);
+  const float rstd = row_scale(a, sum, red);
   if (a.mx) {  // before residual_out is written: it may be residual
     for (int b = threadIdx.x; b < (H >> 5); b += 256) {
       if (a.mx == MOE_MX_FP8_E4M3) norm_block<MOE_MX_FP8_E4M3>(a, t, b, rstd);
