@@ -533,7 +533,7 @@ def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: Ex
     dev = x_codes.device
     f = _mx_fmt(fmt)
     _dense("moe_expert_ffn_mx_codes: x_codes", x_codes, torch.uint8, (T, moe_mx_row_bytes(f, W.hidden)))
-    _dense("moe_expert_ffn_mx_codes: x_scales", x_scales, torch.uint8, (T, W.hidden // 32), dev.index)
+    _dense("moe_expert_ffn_mx_codes: x_scales", x_scales, torch.uint8, (T, W.hidden // 32), x_codes.get_device())
     y = out if out is not None else torch.empty((T * k_total, W.hidden), dtype=torch.float32, device=dev)
     ws = workspace if workspace is not None else _workspace(moe_expert_ffn_mx_workspace_bytes(T, k_total, W, f), dev)
     _check(lib().moe_expert_ffn_mx_codes(_ptr(x_codes), _ptr(x_scales), T, k_total, ctypes.byref(W.c), f,
@@ -545,25 +545,27 @@ def moe_expert_ffn_mx_codes(x_codes: torch.Tensor, x_scales: torch.Tensor, W: Ex
 # ----------------------------------------------------------------------------------------------------
 # In front of the layer.  These calls take few microseconds of GPU time at small T: descriptions are built once, a
 # call checks what its pointers cannot tell and passes plain integers.
-def _dense(what: str, t: torch.Tensor, dtype, shape, index: Optional[int] = -1) -> None:
-    """Contiguous, of this type and shape, and on GPU `index` (-1: anywhere)."""
+def _dense(what: str, t: torch.Tensor, dtype, shape, index: Optional[int] = None) -> None:
+    """Contiguous, of this type and shape, and on GPU `index` (None: anywhere)."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
-    if index != -1 and t.device.index != index:
+    if index is not None and t.get_device() != index:
         raise ValueError(f"{what} must be on GPU {index}, got {t.device}")
 
 
-def _rows(what: str, t: torch.Tensor, T: int, width: int, index: Optional[int]) -> int:
-    """Row stride (in values) of a [T][width] tensor with contiguous rows on GPU `index`."""
-    if t.shape != (T, width) or (t.stride(1) != 1 and width > 1) or t.device.index != index:
-        raise ValueError(f"{what} must be [{T}][{width}] with contiguous rows on GPU {index}, got {tuple(t.shape)} on "
-                         f"{t.device}")
-    return t.stride(0) if T > 1 else width
+def _rows(what: str, t: torch.Tensor, shape, index: int) -> int:
+    """Row stride (in values) of a tensor of shape (rows, width) with contiguous rows on GPU `index` (-1: the CPU)."""
+    if t.shape == shape and t.get_device() == index:
+        far, near = t.stride()
+        if near == 1 or shape[1] <= 1:
+            return far if shape[0] > 1 else shape[1]
+    raise ValueError(f"{what} must be [{shape[0]}][{shape[1]}] with contiguous rows on GPU {index}, got "
+                     f"{tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _on_gpu(what: str, ws: torch.Tensor, index: int) -> None:
-    if ws.device.index != index or ws.dtype is not torch.uint8 or not ws.is_contiguous():
+    if ws.get_device() != index or ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError(f"{what} must be contiguous uint8 on GPU {index}, got {ws.dtype} on {ws.device}")
 
 
@@ -575,8 +577,8 @@ def _dtype(what: str, t: torch.Tensor) -> int:
 
 
 def _gpu(t: torch.Tensor) -> int:
-    index = t.device.index
-    if index is None or not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"needs a GPU tensor, got one on {t.device}")
     return index
 
@@ -611,30 +613,30 @@ class RouteRule:
         self.at = ctypes.addressof(self.c)
 
 
-def _route_out(what: str, rule: RouteRule, T: int, E: int, dev, want_scores: bool, out):
+def _route_out(rule: RouteRule, T: int, E: int, like: torch.Tensor, gpu: int, want_scores: bool, out):
     b = rule.selection_bias
-    if b is not None and (b.numel() != E or b.device != dev):
-        raise ValueError(f"{what}: the selection bias has {b.numel()} values on {b.device}, expected {E} on {dev}")
-    kt = rule.k_total
+    if b is not None and (b.numel() != E or b.get_device() != gpu):
+        raise ValueError(f"the selection bias has {b.numel()} values on {b.device}, expected {E} on GPU {gpu}")
+    shape = (T, rule.k_total)
     if out is None:
-        return (torch.empty((T, kt), dtype=torch.int32, device=dev),
-                torch.empty((T, kt), dtype=torch.float32, device=dev),
+        dev = like.device
+        return (torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.float32, device=dev),
                 torch.empty((T, E), dtype=torch.float32, device=dev) if want_scores else None)
     ids, w, scores = out
-    _dense(f"{what}: ids", ids, torch.int32, (T, kt), dev.index)
-    _dense(f"{what}: weights", w, torch.float32, (T, kt), dev.index)
+    _dense("ids", ids, torch.int32, shape, gpu)
+    _dense("weights", w, torch.float32, shape, gpu)
     if scores is not None:
-        _dense(f"{what}: scores", scores, torch.float32, (T, E), dev.index)
+        _dense("scores", scores, torch.float32, (T, E), gpu)
     return out
 
 
 def moe_select_experts(logits: torch.Tensor, rule: RouteRule, want_scores: bool = False, out=None):
     """The rule on router logits [T][E] (bf16, fp16 or fp32, contiguous rows)
     -> (ids int32 [T][k'], weights fp32 [T][k'], scores fp32 [T][E] or None)."""
-    T, E = logits.shape
+    T, E = shape = logits.shape
     gpu = _gpu(logits)
-    stride = _rows("moe_select_experts: logits", logits, T, E, gpu)
-    ids, w, scores = _route_out("moe_select_experts", rule, T, E, logits.device, want_scores, out)
+    stride = _rows("moe_select_experts: logits", logits, shape, gpu)
+    ids, w, scores = _route_out(rule, T, E, logits, gpu, want_scores, out)
     _enqueue("moe_select_experts", gpu, logits.data_ptr(), _dtype("logits", logits), stride, T, E, rule.at,
              ids.data_ptr(), w.data_ptr(), None if scores is None else scores.data_ptr())
     return ids, w, scores
@@ -645,14 +647,13 @@ def moe_route_grouped(x: torch.Tensor, w_router: torch.Tensor, rule: RouteRule, 
     """The rule on the logits x w_router^T -> (ids, weights, scores) as moe_select_experts."""
     T, H = x.shape
     E = w_router.shape[0]
-    dev = x.device
     gpu = _gpu(x)
     _dense("moe_route_grouped: x", x, x.dtype, (T, H))
     _dense("moe_route_grouped: w_router", w_router, torch.float32, (E, H), gpu)
-    ids, w, scores = _route_out("moe_route_grouped", rule, T, E, dev, want_scores, out)
+    ids, w, scores = _route_out(rule, T, E, x, gpu, want_scores, out)
     ws = workspace
     if ws is None:
-        ws = _workspace(moe_route_workspace_bytes(T, H, E), dev)
+        ws = _workspace(moe_route_workspace_bytes(T, H, E), x.device)
     else:
         _on_gpu("moe_route_grouped: workspace", ws, gpu)
     _enqueue("moe_route_grouped", gpu, x.data_ptr(), _act_dtype(x), T, H, w_router.data_ptr(), E, rule.at,
@@ -678,17 +679,17 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
     without a residual); for mx "fp8", "fp6" or "fp4" the MX codes and scales of y as moe_mx_quantize lays them
     out (None without).  `out` gives the four buffers; a None for y or residual_out there leaves that output
     out, and residual_out may be residual itself."""
-    T, H = x.shape
+    T, H = shape = x.shape
     gpu = _gpu(x)
     f = 0 if mx is None else _mx_fmt(mx)
-    if norm.hidden != H or norm.weight.device.index != gpu:
+    if norm.hidden != H or norm.weight.get_device() != gpu:
         raise ValueError(f"moe_add_rms_norm: rows of {H} values on GPU {gpu}, the weight has {norm.hidden} on "
                          f"{norm.weight.device}")
-    xs = _rows("moe_add_rms_norm: x", x, T, H, gpu)
+    xs = _rows("moe_add_rms_norm: x", x, shape, gpu)
     rp = rop = cp = sp = None
     rs = ros = rdt = 0
     if residual is not None:
-        rs, rdt, rp = (_rows("moe_add_rms_norm: residual", residual, T, H, gpu), _dtype("residual", residual),
+        rs, rdt, rp = (_rows("moe_add_rms_norm: residual", residual, shape, gpu), _dtype("residual", residual),
                        residual.data_ptr())
     if out is None:
         dev = x.device
@@ -701,7 +702,7 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
     else:
         y, ro, codes, scales = out
         if y is not None:
-            _dense("moe_add_rms_norm: y", y, y.dtype, (T, H), gpu)
+            _dense("moe_add_rms_norm: y", y, y.dtype, shape, gpu)
         if f:
             if codes is None or scales is None:
                 raise ValueError("moe_add_rms_norm: mx needs codes and scales")
@@ -711,7 +712,7 @@ def moe_add_rms_norm(x: torch.Tensor, norm: RmsNorm, residual: Optional[torch.Te
         if ro is not None and (residual is None or ro.dtype is not residual.dtype):
             raise ValueError("moe_add_rms_norm: residual_out needs a residual of its type")
     if ro is not None:
-        ros, rop = _rows("moe_add_rms_norm: residual_out", ro, T, H, gpu), ro.data_ptr()
+        ros, rop = _rows("moe_add_rms_norm: residual_out", ro, shape, gpu), ro.data_ptr()
     if f:
         cp, sp = codes.data_ptr(), scales.data_ptr()
     _enqueue("moe_add_rms_norm", gpu, norm.at, x.data_ptr(), _dtype("x", x), xs, rp, rdt, rs, T, rop, ros,
@@ -727,13 +728,14 @@ class LinearWeights:
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, fmt: str = "mxfp4",
                  zeros: Optional[torch.Tensor] = None, tensor_scale: Optional[torch.Tensor] = None):
         self.fmt, self.n_out, self.k_in = W_FORMATS[fmt], codes.shape[0], 2 * codes.shape[1]
+        self.device, self.index = codes.device, codes.get_device()
         K = self.k_in
         p = moe_proj()
 
         def rows(what, t, width):
             if t is None or t.dtype != torch.uint8 or t.shape[0] != self.n_out or t.device != codes.device:
                 raise ValueError(f"LinearWeights: {what} must be uint8 [{self.n_out}][{width}] on {codes.device}")
-            return t.data_ptr(), _rows(f"LinearWeights: {what}", t, self.n_out, width, codes.device.index)
+            return t.data_ptr(), _rows(f"LinearWeights: {what}", t, (self.n_out, width), self.index)
 
         p.w, p.w_row_stride = rows("codes", codes, K // 2)
         p.scales, p.s_row_stride = rows("scales", scales, K // 32 if self.fmt == MOE_W_MXFP4 else K // 16)
@@ -745,7 +747,6 @@ class LinearWeights:
             _dense("LinearWeights: tensor_scale", tensor_scale, torch.float32, (1,))
             p.tensor_scale = tensor_scale.data_ptr()
         self.tensors = (codes, scales, zeros, tensor_scale)
-        self.device, self.index = codes.device, codes.device.index
         self._need = {}  # workspace bytes by T
         self.c = moe_linear_weights(self.fmt, self.n_out, K, p)
         self.at = ctypes.addressof(self.c)
@@ -766,12 +767,12 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
     gpu = _gpu(x)
     if W.index != gpu:
         raise ValueError(f"moe_linear: x is on GPU {gpu}, the weights on {W.device}")
-    xs = _rows("moe_linear: x", x, T, W.k_in, gpu)
+    xs = _rows("moe_linear: x", x, (T, W.k_in), gpu)
     if bias is not None:
         _dense("moe_linear: bias", bias, torch.float32, (W.n_out,), gpu)
     if out is None:
         out = torch.empty((T, W.n_out), dtype=dtype, device=x.device)
-    ys = _rows("moe_linear: out", out, T, W.n_out, gpu)
+    ys = _rows("moe_linear: out", out, (T, W.n_out), gpu)
     ws = workspace
     if ws is None:
         need = moe_linear_workspace_bytes(T, W)
