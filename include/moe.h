@@ -34,8 +34,8 @@
  *  - Validation happens before anything is enqueued; on any error nothing is launched and the
  *    status says why.  T == 0 returns MOE_OK without touching any pointer.
  *  - Inputs are read-only; outputs are overwritten (never accumulated into); buffers must not
- *    alias each other (but moe_add_rms_norm's residual_out may be its residual).  Calls that share no output buffer may run concurrently on different
- *    streams.
+ *    alias each other (but moe_add_rms_norm's residual_out may be its residual).  Calls that share
+ *    no output buffer and no workspace may run concurrently on different streams.
  *  - Results are deterministic: the same inputs give bit-identical outputs on every run (no
  *    floating-point atomics anywhere).
  */

@@ -212,7 +212,8 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
       for (int t = 0; t < TT; ++t) {
         X[t] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) X[t] = __builtin_amdgcn_fdot2_f32_bf16(bitcast<bf16x2>(v[t][i >> 2][i & 3]), one, X[t], false);
+        for (int i = 0; i < 16; ++i)
+          X[t] = __builtin_amdgcn_fdot2_f32_bf16(bitcast<bf16x2>(v[t][i >> 2][i & 3]), one, X[t], false);
       }
     }
     float D[2][TT];
@@ -288,7 +289,7 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
 // both through LDS, and decoding follow one another in each wave, and the registers leave two waves per SIMD.
 template <int FMT, int RT, int MT, int NW>
 __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
-  constexpr int kWave = RT * 2048 + RT * 512 + MT * 4096;  // LDS bytes of a wave: its span of codes and scales, its half span of x
+  constexpr int kWave = RT * 2048 + RT * 512 + MT * 4096;  // a wave's LDS: its span of codes and scales, half span of x
   constexpr int kSlots = NW * kWave, kRed = NW * RT * MT * 1024;
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots > kRed ? kSlots : kRed];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -486,7 +487,8 @@ __device__ __forceinline__ void tile_out(const LinArgs& a, int t, int n, const f
       for (int r = 0; r < RW; ++r) {
         f32x4 v = acc[r][m];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = FMT == MOE_W_NVFP4 ? __builtin_fmaf(v[e], ts, bias[r][e]) : v[e] + bias[r][e];
+        for (int e = 0; e < 4; ++e)
+          v[e] = FMT == MOE_W_NVFP4 ? __builtin_fmaf(v[e], ts, bias[r][e]) : v[e] + bias[r][e];
         store4<DT>(a, t + 16 * m, n + 16 * r, v, vec);
       }
     }

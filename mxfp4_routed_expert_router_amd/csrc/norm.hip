@@ -131,7 +131,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs a) {
 }
 
 // Rows shorter than eight or longer than 32768 values: two passes over the row, one value at a time (the second
-// pass finds it in the caches).  residual_out may be residual itself, so the second pass reads a value before it writes it.
+// pass finds it in the caches).  residual_out may be residual itself, so the second pass reads a value before it
+// writes it.
 template <int F>
 __device__ __forceinline__ void norm_block(const NormArgs& a, int64_t t, int b, float rstd) {
   float y[32];

@@ -27,8 +27,8 @@ namespace {
 constexpr int kSelWaves = 4;  // tokens per workgroup
 
 // Bounds of a score's distance from its exact value, in 2^-24.  Sigmoid (s <= 1): exp 2 s (1 - s) <= 1/2, the
-// addition 1, the reciprocal 2, and some to spare.  Softmax, relative to the largest score p_0 (the scores are p_0 e^-d): the
-// rounded argument d at most d e^-d <= 0.37, exp 2, reciprocal and product 3, the denominator's VPL + 6 additions
+// addition 1, the reciprocal 2, and some to spare.  Softmax, relative to the largest score p_0 (the scores are
+// p_0 e^-d): the rounded argument d at most d e^-d <= 0.37, exp 2, reciprocal and product 3, the denominator's VPL + 6 additions
 // one each and its terms' 2, and some to spare.
 constexpr float kSigmoidUlps = 4.0f, kSoftmaxUlps = 16.0f;  // softmax: plus VPL, times p_0
 constexpr float kEps = 5.9604645e-8f;  // 2^-24
@@ -89,10 +89,11 @@ __device__ __forceinline__ float load_logit(const SelArgs& a, int t, int e) {
 // agree by then), then lane ^ 16, ^ 32.
 template <int STEP>
 __device__ __forceinline__ float group_lane(float v) {
-  if constexpr (STEP == 1) return __uint_as_float(dpp_u32<0xB1, 0xF>(0u, __float_as_uint(v)));        // quad_perm 1,0,3,2
-  else if constexpr (STEP == 2) return __uint_as_float(dpp_u32<0x4E, 0xF>(0u, __float_as_uint(v)));   // quad_perm 2,3,0,1
-  else if constexpr (STEP == 4) return __uint_as_float(dpp_u32<0x141, 0xF>(0u, __float_as_uint(v)));  // row_half_mirror
-  else if constexpr (STEP == 8) return __uint_as_float(dpp_u32<0x140, 0xF>(0u, __float_as_uint(v)));  // row_mirror
+  // quad_perm 1,0,3,2 and 2,3,0,1, row_half_mirror, row_mirror
+  if constexpr (STEP == 1) return __uint_as_float(dpp_u32<0xB1, 0xF>(0u, __float_as_uint(v)));
+  else if constexpr (STEP == 2) return __uint_as_float(dpp_u32<0x4E, 0xF>(0u, __float_as_uint(v)));
+  else if constexpr (STEP == 4) return __uint_as_float(dpp_u32<0x141, 0xF>(0u, __float_as_uint(v)));
+  else if constexpr (STEP == 8) return __uint_as_float(dpp_u32<0x140, 0xF>(0u, __float_as_uint(v)));
   else return __shfl_xor(v, STEP, kWave);
 }
 template <int STEP>
@@ -301,7 +302,8 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelArgs a) {
   if (a.topk_groups < a.n_groups) {
     float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) merge2(m1, m2, (a.group_max && !a.bias && key[v] != -INFINITY) ? L[v] : key[v], -INFINITY);
+    for (int v = 0; v < VPL; ++v)
+      merge2(m1, m2, (a.group_max && !a.bias && key[v] != -INFINITY) ? L[v] : key[v], -INFINITY);
     merge_group(m1, m2, a.lanes);
     const bool one = a.group_max || m2 == -INFINITY;
     const float rank = one ? m1 : m1 + m2;
