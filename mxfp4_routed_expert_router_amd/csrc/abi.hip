@@ -774,7 +774,7 @@ moe_status moe_add_rms_norm(const moe_norm* norm, const void* x, moe_dtype x_dty
 
 size_t moe_linear_workspace_bytes(int T, const moe_linear_weights* W) {
   if (!W || T <= 0 || W->n_out <= 0 || W->k_in <= 0) return 0;
-  return round_up(moe::linear_workspace_bytes(T, W->n_out, W->k_in), 256);
+  return round_up(moe::linear_workspace_bytes(W->fmt, T, W->n_out, W->k_in), 256);
 }
 
 moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride, int T, const moe_linear_weights* W,

@@ -163,7 +163,7 @@ struct LinArgs {
   int64_t y_stride;
   void* ws;
 };
-size_t linear_workspace_bytes(int T, int N, int K);
+size_t linear_workspace_bytes(int fmt, int T, int N, int K);
 hipError_t launch_linear(const LinArgs& a, hipStream_t stream);
 
 // ---- combine ----

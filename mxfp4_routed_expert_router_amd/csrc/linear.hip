@@ -274,7 +274,7 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
   }
 }
 
-// ---- few tokens: the weights stream once, 16 RT rows per workgroup, its NW waves share K in whole spans ----
+// ---- few tokens: the weights stream, 16 RT rows x 16 MT tokens per workgroup, its NW waves share K in whole spans ----
 // A span is 256 values of K: 128 bytes of codes per row, so a load instruction (8 rows x 128 bytes) takes whole
 // lines, with the nontemporal hint (a line is used once; the lines of the 16-row x 64-byte shape that the MFMA
 // layout would give read about 13% slower from HBM, and lanes that are neighbours in different rows cost the
@@ -294,14 +294,14 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kSlots > kRed ? kSlots : kRed];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l16 = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
-  const int n0 = blockIdx.x * 16 * RT;
+  const int n0 = blockIdx.x * 16 * RT, t0 = blockIdx.y * 16 * MT;
   const int blocks = a.K / 32, spans = (a.K + kSpan - 1) / kSpan;
   const int p0 = (int)((int64_t)spans * wave / NW), p1 = (int)((int64_t)spans * (wave + 1) / NW);
   // Buffer descriptors end with the last row's last value.  Only a load's per-lane offset is checked against them,
   // so that offset holds the row (rows past N and tokens past T lie past the end: zeros) and is put out of range
   // for a lane past K or past the wave's share; the uniform offset adds the place in K, inside the row for the rest.
   constexpr int kPer = FMT == MOE_W_MXFP4 ? 1 : 2;  // scale bytes per block
-  const int rows = min(16 * RT, a.N - n0);
+  const int rows = min(16 * RT, a.N - n0), toks = min(16 * MT, a.T - t0);
   const __amdgpu_buffer_rsrc_t wr =
       make_rsrc(a.w.w + (int64_t)n0 * a.w.wr, (int64_t)(rows - 1) * a.w.wr + a.K / 2);
   const __amdgpu_buffer_rsrc_t sr =
@@ -309,7 +309,8 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
   const __amdgpu_buffer_rsrc_t zr =
       FMT == MOE_W_INT4_G32 ? make_rsrc(a.w.z + (int64_t)n0 * a.w.zr, (int64_t)(rows - 1) * a.w.zr + (blocks + 1) / 2)
                             : sr;
-  const __amdgpu_buffer_rsrc_t xr = make_rsrc(a.x, ((int64_t)(a.T - 1) * a.x_stride + a.K) * 2);  // T <= 16 MT
+  const __amdgpu_buffer_rsrc_t xr =
+      make_rsrc(a.x + (int64_t)t0 * a.x_stride, ((int64_t)(toks - 1) * a.x_stride + a.K) * 2);
   const uint32_t woff = (uint32_t)(lr * a.w.wr) + 16u * lc;
   const uint32_t soff = (uint32_t)(lr * a.w.sr) + kPer * lc, zoff = (uint32_t)(lr * a.w.zr) + (lc >> 1);
   const uint32_t xoff = (uint32_t)(q * a.x_stride) * 2u + 16u * l16;  // token 4 i + q, piece l16 of a half span
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
     for (int w = 1; w < NW; ++w) v += red[w * RT * MT * 64 + i];
     const int l = i & 63, m = (i >> 6) % MT, r = i / (64 * MT);
     const int t = 16 * m + (l & 15), n = n0 + 16 * r + 4 * (l >> 4);
-    if (t < a.T) store_out<FMT>(a, t, n, v, ts);
+    if (t < toks) store_out<FMT>(a, t0 + t, n, v, ts);
   }
 }
 
@@ -633,9 +634,9 @@ __global__ __launch_bounds__(256, 2) void linear_tile_kernel(LinArgs a, int t_ti
   else tile_out<FMT, MOE_DT_FP16>(a, t0 + tw + l16, nw + 4 * q, acc, bias, ts, vec);
 }
 
-// y = the partial sums of the splits in order, with the tensor scale and the bias.  All of a thread's loads are
+// y = the partial sums of the splits in order, with the tensor scale and the bias.  Eight loads of a thread are
 // issued before the first addition (one after another they took 11 us for 128 tokens x 7168, eight splits).
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 32;
 template <int FMT>
 __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -646,12 +647,15 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits)
   const int64_t plane = (int64_t)a.T * a.N;
   const float ts = FMT == MOE_W_NVFP4 ? *a.w.ts : 1.0f;
   if (n + 4 <= a.N) {
-    f32x4 v[kMaxSplits], sum = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 8;
+    f32x4 v[kBatch], sum = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < splits; s0 += kBatch) {
 #pragma unroll
-    for (int s = 0; s < kMaxSplits; ++s) __builtin_memcpy(&v[s], p + min(s, splits - 1) * plane, 16);
+      for (int s = 0; s < kBatch; ++s) __builtin_memcpy(&v[s], p + min(s0 + s, splits - 1) * plane, 16);
 #pragma unroll
-    for (int s = 0; s < kMaxSplits; ++s)
-      if (s < splits) sum += v[s];
+      for (int s = 0; s < kBatch; ++s)
+        if (s0 + s < splits) sum += v[s];
+    }
     store_out<FMT>(a, t, n, sum, ts);
   } else {  // the last columns of a row
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
@@ -673,35 +677,46 @@ void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
   else linear_dot_kernel<FMT, TT, 4><<<g, 256, 0, stream>>>(a);
 }
 
-// Rows per workgroup: every workgroup reads all of x, so as many as leave about 200 workgroups (one per CU).  16
-// tokens, 7168 rows x 7168: 16 rows 14.5 us, 32 rows 12.6; 2048 rows: 8.3 and 11.1; 32 tokens, 16384 rows x 4096:
-// 33.5, 20.4 and 64 rows 17.3.  Eight waves, four where their LDS does not fit (64 tokens and more than 16 rows).
-template <int FMT, int MT, int RT>
-void launch_stream_rows(const LinArgs& a, hipStream_t stream) {
-  constexpr int NW = MT == 4 && RT > 1 ? 4 : 8;
-  linear_stream_kernel<FMT, RT, MT, NW><<<dim3((unsigned)((a.N + 16 * RT - 1) / (16 * RT))), 64 * NW, 0, stream>>>(a);
+// Rows (16 rt) and tokens (16 mt) of a streaming workgroup: the fewest that leave at most one workgroup per CU, since
+// those of a second round start when the first have ended (32 tokens x 4096 MXFP4: 4096 rows 8.0 us, 4500 rows 13.8
+// with 16 rows a workgroup and 9.5 with 32; 8192 rows 10.2 with 32, 8838 rows 16.9, and 13.4 with 64).  More than 32
+// tokens take a workgroup per 32 or 64 of them and rows, in place of tiles (mt 0), while one round holds them all and
+// K is not long, since then a tile's steps and the join of its shares wait for their loads (us, streamed and tiles:
+// 135 x 257 x 1728 INT4 5.6 and 15.1, 256 x 1024 x 2048 MXFP4 7.0 and 11.6, 128 x 4096 x 4096 13.3 and 18.9, 512 x
+// 2048 x 7168 30.3 and 32.1; K = 9248 18.1 and 21.8, 16384 20.8 and 19.3).  64 rows x 64 tokens of INT4, four waves
+// with two products per weight, only to K = 4096 (512 x 2048 x 1024 13.1 and 17.9, 100 x 6144 x 4096 30.8 and 29.6,
+// 40 x 8838 x 7296 55 and 38).
+constexpr int kCus = 256;
+struct StreamPlan {
+  int rt, mt;
+};
+StreamPlan stream_plan(int fmt, int T, int N, int K) {
+  if (T <= 16) return {N <= 16 * kCus ? 1 : N <= 32 * kCus ? 2 : 4, 1};
+  if (T > 32 && K > 12288) return {0, 0};
+  constexpr StreamPlan sizes[] = {{1, 2}, {2, 2}, {4, 2}, {4, 4}};
+  for (const StreamPlan& p : sizes) {
+    const int64_t groups = (int64_t)((N + 16 * p.rt - 1) / (16 * p.rt)) * ((T + 16 * p.mt - 1) / (16 * p.mt));
+    if (groups <= kCus && !(p.mt == 4 && fmt == MOE_W_INT4_G32 && K > 4096)) return p;
+  }
+  return T <= 32 ? StreamPlan{4, 2} : StreamPlan{0, 0};
 }
-template <int FMT, int MT>
-void launch_stream_tokens(const LinArgs& a, hipStream_t stream) {
-  if (a.N >= 64 * 200) launch_stream_rows<FMT, MT, 4>(a, stream);
-  else if (a.N >= 32 * 200) launch_stream_rows<FMT, MT, 2>(a, stream);
-  else launch_stream_rows<FMT, MT, 1>(a, stream);
+// Eight waves, four where their LDS does not fit (64 rows and 64 tokens).
+template <int FMT, int RT, int MT>
+void launch_stream(const LinArgs& a, hipStream_t stream) {
+  constexpr int NW = RT * MT == 16 ? 4 : 8;
+  const dim3 g((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.T + 16 * MT - 1) / (16 * MT)));
+  linear_stream_kernel<FMT, RT, MT, NW><<<g, 64 * NW, 0, stream>>>(a);
 }
 
-// Up to 32 tokens stream the weights, and up to 64 while a wave's share of K is short: tiles share K over workgroups,
-// 64 tokens x 2048 rows x 4096 MXFP4 streamed 12.2 us, 14.0 as tiles; x 5120 14.7 and 14.1; x 7168 18.4 and 15.2;
-// 48 x 2048 x 16384 31.6 and 23.1.  From 6400 rows on (32 rows a workgroup) 7168 x 7168 20.7 and 22.4, 7168 x 16384
-// 40.6 and 35.6.
-bool streams(int T, int N, int K) { return T <= 32 || (T <= 64 && K <= (N < 32 * 200 ? 5120 : 8192)); }
 // Three and four tokens: dot products up to this many rows, where the streaming kernel has fewer than 200 workgroups
 // (4 tokens, 2048 x 7168 MXFP4: 6.1 us, streamed 7.5; 4096 x 4096: 5.9 and 5.6; 7168 x 7168: 13.7 and 10.2).  Two
 // tokens are faster by dot products at every size (7168 x 7168 MXFP4 9.1 us and 9.8, INT4 13.0 and 17.3).
 constexpr int kDotRows = 16 * 200;
 
 // Tiles and K shares of the tile kernel.  128-token tiles where they give a workgroup per CU (2048 tokens x 4096 x
-// 7168 MXFP4: 125 us, 156 with 64), 64-token ones below (128 tokens x 2048 x 7168: 17 us, 21 with 128).  K is shared
-// until there are up to two workgroups per CU, at least a span each (200 tokens x 230 x 1632 INT4: 15.7 us, 17.9
-// with two), unless the tiles alone come near one per CU (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
+// 7168 MXFP4: 118 us, 156 with 64), 64-token ones below.  K is shared over up to 32 workgroups, at least a span each,
+// until there are up to two workgroups per CU (60 tokens x 65 x 13088 INT4: 19.8 us, 22.1 with 16, 29.1 with 8),
+// unless the tiles alone come near one per CU (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
 struct TilePlan {
   int mtw, t_tiles, n_tiles, splits;
 };
@@ -717,16 +732,7 @@ TilePlan tile_plan(int T, int N, int K) {
 }
 
 template <int FMT>
-hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
-  if (streams(a.T, a.N, a.K)) {
-    if (a.T == 1) launch_dot_tokens<FMT, 1>(a, stream);
-    else if (a.T == 2) launch_dot_tokens<FMT, 2>(a, stream);
-    else if (a.T <= 4 && a.N <= kDotRows) launch_dot_tokens<FMT, 4>(a, stream);
-    else if (a.T <= 16) launch_stream_tokens<FMT, 1>(a, stream);
-    else if (a.T <= 32) launch_stream_tokens<FMT, 2>(a, stream);
-    else launch_stream_tokens<FMT, 4>(a, stream);
-    return hipGetLastError();
-  }
+hipError_t linear_tiles(const LinArgs& a, hipStream_t stream) {
   const TilePlan p = tile_plan(a.T, a.N, a.K);
   const int64_t g = (int64_t)p.t_tiles * p.n_tiles * p.splits;
   if (g > 0x7FFFFF) return hipErrorInvalidConfiguration;  // (more than 2^31 threads)
@@ -741,10 +747,27 @@ hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int FMT>
+hipError_t linear_fmt(const LinArgs& a, hipStream_t stream) {
+  const StreamPlan s = stream_plan(FMT, a.T, a.N, a.K);
+  if (a.T == 1) launch_dot_tokens<FMT, 1>(a, stream);
+  else if (a.T == 2) launch_dot_tokens<FMT, 2>(a, stream);
+  else if (a.T <= 4 && a.N <= kDotRows) launch_dot_tokens<FMT, 4>(a, stream);
+  else if (s.mt == 0) return linear_tiles<FMT>(a, stream);
+  else if (s.mt == 4) launch_stream<FMT, 4, 4>(a, stream);
+  else if (s.mt == 2 && s.rt == 4) launch_stream<FMT, 4, 2>(a, stream);
+  else if (s.mt == 2 && s.rt == 2) launch_stream<FMT, 2, 2>(a, stream);
+  else if (s.mt == 2) launch_stream<FMT, 1, 2>(a, stream);
+  else if (s.rt == 4) launch_stream<FMT, 4, 1>(a, stream);
+  else if (s.rt == 2) launch_stream<FMT, 2, 1>(a, stream);
+  else launch_stream<FMT, 1, 1>(a, stream);
+  return hipGetLastError();
+}
+
 }  // namespace
 
-size_t linear_workspace_bytes(int T, int N, int K) {
-  if (streams(T, N, K)) return 0;
+size_t linear_workspace_bytes(int fmt, int T, int N, int K) {
+  if (stream_plan(fmt, T, N, K).mt != 0) return 0;
   const TilePlan p = tile_plan(T, N, K);
   return p.splits > 1 ? sizeof(float) * (size_t)p.splits * (size_t)T * (size_t)N : 0;
 }

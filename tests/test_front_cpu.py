@@ -135,11 +135,13 @@ def test_linear_refusals(fmt):
     if fmt == m.MOE_W_NVFP4:
         assert f(D(tensor_scale=None)) == NULL and f(D(tensor_scale=P + 2)) == ALIGN
     assert L.moe_linear_workspace_bytes(4, ctypes.byref(D())) == 0
-    wide = D(k_in=4096, w_row_stride=2048, s_row_stride=256, **({"z_row_stride": 64} if fmt == m.MOE_W_INT4_G32 else {}))
+    # K = 16384 is shared over workgroups, which takes a workspace
+    wide = D(k_in=16384, w_row_stride=8192, s_row_stride=1024,
+             **({"z_row_stride": 256} if fmt == m.MOE_W_INT4_G32 else {}))
     need = L.moe_linear_workspace_bytes(200, ctypes.byref(wide))
     assert need >= 4 * 200 * 32
-    assert f(wide, T=200, xs=4096, ws=None) == WORKSPACE and f(wide, T=200, xs=4096, wsb=need - 1) == WORKSPACE
-    assert f(wide, T=200, xs=4096, ws=fake(0x8008)) == ALIGN
+    assert f(wide, T=200, xs=16384, ws=None) == WORKSPACE and f(wide, T=200, xs=16384, wsb=need - 1) == WORKSPACE
+    assert f(wide, T=200, xs=16384, ws=fake(0x8008)) == ALIGN
     assert L.moe_linear_workspace_bytes(4, None) == 0 and L.moe_linear_workspace_bytes(0, ctypes.byref(D())) == 0
 
 

@@ -88,10 +88,10 @@ def test_each_call_in_a_graph(T):
 
 def test_two_graphs_on_one_workspace():
     """Products that share K over workgroups, captured twice with one workspace and replayed in turn."""
-    T, W = 150, linear_weights(384, 4096)
+    T, W = 150, linear_weights(384, 16384)
     ws = torch.empty(moe.moe_linear_workspace_bytes(T, W), dtype=torch.uint8, device=DEV)
     assert ws.numel() > 0
-    xs = [rand(T, 4096, seed=s).bfloat16().to(DEV) for s in (1, 2)]
+    xs = [rand(T, 16384, seed=s).bfloat16().to(DEV) for s in (1, 2)]
     outs = [torch.zeros(T, 384, device=DEV) for _ in xs]
     moe.moe_linear(xs[0], W, out=outs[0], workspace=ws)
     torch.cuda.synchronize()

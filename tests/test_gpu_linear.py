@@ -106,7 +106,12 @@ def test_many_rows(fmt, T, N):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("T,N,K", [(4, 3200, 96), (4, 3201, 96), (33, 70, 5120), (33, 70, 5152), (64, 130, 8192),
-                                   (64, 6400, 5152), (50, 6420, 8192), (40, 6403, 8224), (32, 40, 9216)])
+                                   (64, 6400, 5152), (50, 6420, 8192), (40, 6403, 8224), (32, 40, 9216),
+                                   (16, 4096, 96), (10, 4097, 96), (16, 8192, 64), (5, 8193, 64), (32, 4096, 96),
+                                   (17, 4097, 96), (20, 8193, 64), (31, 16385, 64), (33, 2048, 288), (65, 1366, 288),
+                                   (129, 777, 544), (257, 910, 320), (513, 500, 288), (1025, 1000, 96),
+                                   (1024, 1024, 4096), (1000, 1010, 4128), (40, 100, 12288), (35, 100, 12320),
+                                   (2100, 33, 64), (300, 20, 12000)])
 def test_where_kernels_meet(fmt, T, N, K):
     check(T, N, K, fmt)
 
