@@ -715,8 +715,10 @@ constexpr int kDotRows = 16 * 200;
 
 // Tiles and K shares of the tile kernel.  128-token tiles where they give a workgroup per CU (2048 tokens x 4096 x
 // 7168 MXFP4: 118 us, 156 with 64), 64-token ones below.  K is shared over up to 32 workgroups, at least a span each,
-// until there are up to two workgroups per CU (60 tokens x 65 x 13088 INT4: 19.8 us, 22.1 with 16, 29.1 with 8),
-// unless the tiles alone come near one per CU (1024 tokens x 2048 x 2048: 20 us, 24 with two shares).
+// until there are up to two workgroups per CU (60 tokens x 65 x 13088 INT4: 19.8 us, 22.1 with 16, 29.1 with 8); at
+// least five spans each from 128 tiles on (440 tokens x 2714 x 1024 NVFP4: 17.3 us, 24.5 with three shares; 512 x
+// 2048 x 7168 INT4: 49 with four, 57 with three); not at all where the tiles alone come near one per CU (1024 tokens x
+// 2048 x 2048: 20 us, 24 with two shares).
 struct TilePlan {
   int mtw, t_tiles, n_tiles, splits;
 };
@@ -726,7 +728,8 @@ TilePlan tile_plan(int T, int N, int K) {
   p.mtw = (int64_t)((T + 127) / 128) * p.n_tiles >= 256 ? 4 : 2;
   p.t_tiles = (T + 32 * p.mtw - 1) / (32 * p.mtw);
   const int64_t tiles = (int64_t)p.t_tiles * p.n_tiles;
-  const int64_t most = tiles >= 192 ? 1 : std::min<int64_t>(kMaxSplits, std::max(1, K / kSpan));
+  const int64_t most =
+      tiles >= 192 ? 1 : std::min<int64_t>(kMaxSplits, std::max(1, K / (tiles >= 128 ? 5 * kSpan : kSpan)));
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, 512 / tiles));
   return p;
 }
