@@ -472,7 +472,7 @@ moe_status moe_add_rms_norm(const moe_norm *norm, const void *x, moe_dtype x_dty
  *   y    [T] rows of n_out values (bf16, fp16 or fp32), y_row_stride values apart (>= n_out), aligned to a value
  *   workspace moe_linear_workspace_bytes(T, W) bytes, 16-byte aligned (NULL if that is 0)
  * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^24 bytes or more, an x row stride of
- * 2^23 values or more, or n_out > 2^26), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
+ * 2^23 values or more, T > 2^30, or n_out > 2^26), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
 typedef struct {
   moe_w_format fmt;
   int n_out, k_in;

@@ -667,6 +667,7 @@ moe_status moe_route_bucket(const void* x, moe_act_dtype x_dtype, int T, int H, 
 // What stands in front of the layer: residual addition and norm, routing by a rule, 4-bit products.
 namespace {
 
+constexpr int kMostLinearRows = 1 << 30;  // of x (and, for the query, of W): the plans add to them in 32 bits
 inline int dt_bytes(int dt) { return dt == MOE_DT_FP32 ? 4 : 2; }
 inline bool known_dt(int dt) { return dt == MOE_DT_BF16 || dt == MOE_DT_FP16 || dt == MOE_DT_FP32; }
 inline bool al_value(const void* p, int dt) { return ((uintptr_t)p & (uintptr_t)(dt_bytes(dt) - 1)) == 0; }
@@ -773,7 +774,7 @@ moe_status moe_add_rms_norm(const moe_norm* norm, const void* x, moe_dtype x_dty
 }
 
 size_t moe_linear_workspace_bytes(int T, const moe_linear_weights* W) {
-  if (!W || T <= 0 || W->n_out <= 0 || W->k_in <= 0) return 0;
+  if (!W || T <= 0 || T > kMostLinearRows || W->n_out <= 0 || W->n_out > kMostLinearRows || W->k_in <= 0) return 0;
   return round_up(moe::linear_workspace_bytes(W->fmt, T, W->n_out, W->k_in), 256);
 }
 
@@ -782,7 +783,7 @@ moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride
                       size_t workspace_bytes, void* stream) {
   if (T == 0) return MOE_OK;
   if (!W) return MOE_ERR_NULL;
-  if (T < 0 || W->n_out < 1 || W->k_in < 1) return MOE_ERR_SHAPE;
+  if (T < 0 || T > kMostLinearRows || W->n_out < 1 || W->k_in < 1) return MOE_ERR_SHAPE;
   if (!known_format(W->fmt) || W->fmt == MOE_W_FP16 || x_dtype != MOE_ACT_BF16 || !known_dt(y_dtype))
     return MOE_ERR_DTYPE;
   if (!x || !y) return MOE_ERR_NULL;

@@ -124,7 +124,7 @@ def test_linear_refusals(fmt):
     assert f(x=None) == NULL and f(y=None) == NULL and f(D(w=None)) == NULL and f(D(scales=None)) == NULL
     for bad in (dict(T=-1), dict(xs=56), dict(ys=31), dict(xs=1 << 62), dict(xs=1 << 23), dict(ys=1 << 62),
                 dict(d=D(s_row_stride=1 << 24)), dict(d=D(n_out=0)), dict(d=D(k_in=0)),
-                dict(d=D(n_out=(1 << 26) + 1), ys=1 << 27),
+                dict(d=D(n_out=(1 << 26) + 1), ys=1 << 27), dict(T=(1 << 30) + 1), dict(T=(1 << 31) - 1),
                 dict(d=D(w_row_stride=16)), dict(d=D(s_row_stride=1)), dict(d=D(w_row_stride=1 << 24))):
         assert f(**bad) == SHAPE, bad
     assert f(D(k_in=48)) == BLOCK and f(D(w=P + 8)) == BLOCK and f(D(w_row_stride=40)) == BLOCK
