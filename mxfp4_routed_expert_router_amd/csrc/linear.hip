@@ -110,9 +110,11 @@ __device__ __forceinline__ void store_out(const LinArgs& a, int t, int n, f32x4 
 // lines (nontemporal: used once).  A span of x (512 bytes a token) is loaded as it lies, two tokens per instruction,
 // and passes through LDS of the wave's own to the lanes that need its blocks: loaded in the lanes' order (16 bytes
 // every 64) it took four instructions a token and bound the kernel.  Codes are unpacked to bf16 pairs of small exact
-// integers or E2M1 values, two products per v_dot2_f32_bf16; the block's sum D then takes its scale in fp32:
-//   MXFP4, NVFP4  acc += s D       INT4  acc += s (D - z X), X = the sum of the block's x
-// (an unsigned 4-bit code c as an E4M3 byte is c 2^-9 for every c, so INT4 codes unpack by the 8-bit conversion).
+// integers or E2M1 values, two products per v_dot2_f32_bf16; the block's sum D then takes its scale s in fp32:
+// acc += s D.  INT4 codes have their zero point subtracted before the products: c - z is exact in bf16, while
+// D - z sum(x) carries the roundings of c x into weights that are zero.  (A 4-bit code c as an E4M3 byte is c 2^-9
+// for every c, so codes unpack by the 8-bit conversion.  7168 x 7168 INT4: 11.2 us with the subtraction and 10.5 with
+// sum(x) for one token, 13.0 and 13.3 for two; 4 x 3200 x 4096 6.7 and 7.1.)
 // Bound: one token x 7168 x 7168 MXFP4 reads its 27.3 MB in 7.8 us (3.5 TB/s; of which about 3 us are a launch and
 // the first loads' latency); from three tokens on by the vector ALU (4 tokens of that size 13.7 us).
 constexpr int kSpan = 256;
@@ -121,16 +123,19 @@ struct DotScale {
   uint32_t s, z;
 };
 
-// Eight codes of dword d as four bf16 pairs (k ascending).
+// Eight codes of dword d as four bf16 pairs (k ascending), less z for INT4.
 template <int FMT>
-__device__ __forceinline__ void unpack_pairs(uint32_t d, bf16x2 (&w)[4]) {
+__device__ __forceinline__ void unpack_pairs(uint32_t d, float z, bf16x2 (&w)[4]) {
   if constexpr (FMT == MOE_W_INT4_G32) {
     const uint32_t even = d & 0x0F0F0F0Fu, odd = (d >> 4) & 0x0F0F0F0Fu;
-    const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u), b = __builtin_amdgcn_perm(odd, even, 0x07030602u);
-    w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false);
-    w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true);
-    w[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false);
-    w[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true);
+    const f32x2 e0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.0f, false);
+    const f32x2 e1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(even, 512.0f, true);
+    const f32x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.0f, false);
+    const f32x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(odd, 512.0f, true);
+    w[0] = bitcast<bf16x2>(pack_high(e0[0] - z, o0[0] - z));
+    w[1] = bitcast<bf16x2>(pack_high(e0[1] - z, o0[1] - z));
+    w[2] = bitcast<bf16x2>(pack_high(e1[0] - z, o1[0] - z));
+    w[3] = bitcast<bf16x2>(pack_high(e1[1] - z, o1[1] - z));
   } else {
     w[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0);
     w[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 1);
@@ -205,24 +210,15 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[t][i] = ld16(xr + 512 * t + 16 * (i ^ (lc >> 2)));
     fence();
-    float X[TT];
-    if constexpr (FMT == MOE_W_INT4_G32) {
-      const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        X[t] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          X[t] = __builtin_amdgcn_fdot2_f32_bf16(bitcast<bf16x2>(v[t][i >> 2][i & 3]), one, X[t], false);
-      }
-    }
+    // zero point of block 8 p + lc, whose parity is lc's
+    const float z = FMT == MOE_W_INT4_G32 ? (float)((s.z >> (4 * (lc & 1))) & 15u) : 0.0f;
     float D[2][TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) D[0][t] = D[1][t] = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       bf16x2 w[4];
-      unpack_pairs<FMT>(c[i], w);
+      unpack_pairs<FMT>(c[i], z, w);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -235,9 +231,7 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
       if constexpr (FMT == MOE_W_MXFP4) {
         o = e8m0_to_f32(s.s) * (D[0][t] + D[1][t]);
       } else if constexpr (FMT == MOE_W_INT4_G32) {
-        const int b = 8 * p + lc;
-        const float z = (float)((s.z >> (4 * (b & 1))) & 15u);
-        o = (float)bitcast<_Float16>((uint16_t)s.s) * __builtin_fmaf(-z, X[t], D[0][t] + D[1][t]);
+        o = (float)bitcast<_Float16>((uint16_t)s.s) * (D[0][t] + D[1][t]);
       } else {
         o = __builtin_fmaf(e4m3_value(s.s & 255u), D[0][t], e4m3_value(s.s >> 8) * D[1][t]);
       }

@@ -196,3 +196,42 @@ def test_empty_batch():
     codes, scales, _, _, _ = ref.weights("mxfp4", 8, 64, rng)
     assert moe.moe_linear(torch.empty(0, 64, dtype=torch.bfloat16, device=DEV),
                           moe.LinearWeights(dev(codes), dev(scales))).shape == (0, 8)
+
+
+def int4_weights(codes, zeros, scales):
+    """LinearWeights of codes [N][K] and zero points [N][K/32] (four bits each) and binary16 scales [N][K/32]; and
+    the decoded matrix in 64 bits."""
+    N, K = codes.shape
+    packed = (codes[:, 0::2] | codes[:, 1::2] << 4).astype(np.uint8)
+    z = np.pad(zeros, ((0, 0), (0, zeros.shape[1] % 2)))
+    zp = (z[:, 0::2] | z[:, 1::2] << 4).astype(np.uint8)
+    h = scales.astype(np.float16)
+    w = (codes.astype(np.float64) - np.repeat(zeros, 32, 1)) * np.repeat(h.astype(np.float64), 32, 1)
+    return moe.LinearWeights(dev(packed), dev(h.view(np.uint8).reshape(N, K // 16)), "int4g32", dev(zp)), w
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 20, 150])
+@pytest.mark.parametrize("N,K", [(40, 4096), (2100, 288), (3210, 96)])
+def test_int4_codes_at_their_zero_point(T, N, K):
+    """Weights that are exactly zero add exactly nothing: rows of nothing else give 0 (or the bias), and the largest
+    channels of x add no rounding where their code is the zero point."""
+    rng = np.random.default_rng(T + N)
+    zeros = rng.integers(0, 16, (N, K // 32))
+    codes = np.repeat(zeros, 32, 1)
+    x = torch.from_numpy(rng.standard_normal((T, K))).bfloat16()
+    b = rng.standard_normal(N).astype(np.float32)
+    W, _ = int4_weights(codes, zeros, rng.uniform(0.005, 0.02, zeros.shape))
+    assert not bool(moe.moe_linear(x.to(DEV), W).any())
+    assert torch.equal(moe.moe_linear(x.to(DEV), W, dev(b)).cpu(), torch.from_numpy(b).expand(T, N))
+    # one channel of each block 3000 times the others, its code the zero point; some of the other weights +-1 step
+    step = rng.integers(-1, 2, (N, K)) * (rng.random((N, K)) < 0.2)
+    big = np.arange(0, K, 32) + rng.integers(0, 32, K // 32)
+    step[:, big] = 0
+    codes = np.clip(codes + step, 0, 15)
+    x[:, big] *= 3000
+    W, w = int4_weights(codes, zeros, rng.uniform(0.005, 0.02, zeros.shape))
+    xs = x.double().numpy()
+    want = xs @ w.T
+    got = moe.moe_linear(x.to(DEV), W).double().cpu().numpy()
+    bad = ~(np.abs(got - want) <= ref.linear_tolerance(xs, w, K, want, "fp32"))
+    assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
