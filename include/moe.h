@@ -168,7 +168,7 @@ moe_status moe_route_sigmoid(const void *x, moe_act_dtype x_dtype, int T, int H,
  *   slots     j = 0 .. top_k-1 hold the available experts of those groups by (key descending, index
  *             ascending), weights[t,j] = routed_scale * s_j, divided by the sum of the selected s if
  *             renormalise.  Where fewer than top_k are left, the other slots get id -1 and weight 0 (as
- *             moe_pad_rows marks them: moe_bucket drops them).  A sum of scores that underflows fp32 gives
+ *             moe_pad_rows marks them: moe_bucket drops them, moe_combine leaves them out).  A sum of scores that underflows fp32 gives
  *             weights of 0;
  *   shared    slots top_k .. top_k+n_shared-1 hold experts E .. E+n_shared-1 with weight shared_weight.
  * The choice is that of the keys in 64 bits, also where two keys or ranks are closer than fp32 can
@@ -361,6 +361,7 @@ moe_status moe_expert_ffn_f16(const void *x, moe_act_dtype x_dtype, int T, int k
  * in ascending j),
  *   y~[t,:] = binary16(sum_{j ascending} (weights[t,j] / F_t) * y_slots[t*k_total+j,:])  (fp32 sum)
  *   y[t,:]  = A * F_t * y~[t,:]                                                      (fp32, exact)
+ * A slot of weight 0 adds nothing, whatever its row holds.
  * y_slots [T*k_total][H] binary16 (8-byte aligned), weights [T][k_total] fp32, y [T][H] fp32 out
  * (16-byte aligned), H % 4 == 0.  Errors: NULL, SHAPE (also attenuation_log2 out of range), ALIGN,
  * HIP. */
@@ -486,7 +487,8 @@ moe_status moe_linear(const void *x, moe_act_dtype x_dtype, int64_t x_row_stride
 /* ---------------------------------------------------------------------------------------------
  * moe_combine -- weighted reduction [C31] with FP32 output [C32]:
  *   y[t,:] = sum_{j = 0 .. k_total-1, in ascending j} weights[t,j] * y_slots[t*k_total+j,:]
- * Every output element has exactly one owner (no atomics).
+ * Every output element has exactly one owner (no atomics).  A slot of weight 0 adds nothing, whatever
+ * its row holds: rows of dropped slots are not written by the expert FFN.
  *   y_slots [T*k_total][H] fp32, weights [T][k_total] fp32, y [T][H] fp32 out; H % 4 == 0,
  *   y_slots and y 16-byte aligned.
  * Errors: NULL, SHAPE, ALIGN, HIP. */

@@ -852,9 +852,9 @@ class MoEBlock:
 
     forward(attn, residual) -> (y fp32 [T][H], residual_out): the next block's norm adds y to residual_out.
 
-    Whether the rule's selection_bias can leave slots empty (a value of -inf) is read when the block is built: a
-    bias that masks experts only later needs a new block.  Passes of one block share its buffers, so they run one
-    after another on one stream."""
+    Slots that a bias or logits that are not finite leave empty add nothing; a token none of whose logits is finite
+    (NaN in its row) gets its shared experts alone.  Passes of one block share its buffers, so they run one after
+    another on one stream."""
 
     def __init__(self, W: ExpertWeights, T: int, rule: RouteRule, w_router: torch.Tensor, norm: RmsNorm,
                  W_o: Optional[LinearWeights] = None, mx=None):
@@ -882,10 +882,9 @@ class MoEBlock:
                                torch.empty(n, dtype=torch.int32, device=dev),
                                torch.empty(n, dtype=torch.int32, device=dev))
         self.bucket_ws = _workspace(moe_bucket_workspace_bytes(n, W.n_experts), dev)
-        # A bias of -inf may leave slots empty (id -1, weight 0).  The FFN does not write their rows, and 0 times
-        # what an earlier pass left there could be NaN: such a rule clears the rows in every pass.
+        # whether the bias masks experts, so that slots may stay empty in every pass
         self.clear = rule.selection_bias is not None and not bool(torch.isfinite(rule.selection_bias).all())
-        self.y_slots = torch.zeros((n, H), dtype=torch.float32, device=dev)
+        self.y_slots = torch.empty((n, H), dtype=torch.float32, device=dev)
         self.ffn_ws = _workspace(moe_expert_ffn_workspace_bytes(T, kt, W) if self.mx is None
                                  else moe_expert_ffn_mx_workspace_bytes(T, kt, W, self.mx), dev)
         self.y = torch.empty((T, H), dtype=torch.float32, device=dev)
@@ -902,8 +901,6 @@ class MoEBlock:
         moe_route_grouped(self.x, self.w_router, self.rule, out=(self.ids, self.weights, None),
                           workspace=self.route_ws)
         b = moe_bucket(self.ids, self.W.n_experts, out=self.buckets, workspace=self.bucket_ws)
-        if self.clear:
-            self.y_slots.zero_()
         if self.mx is None:
             moe_expert_ffn(self.x, self.W, b.offsets, b.sorted_slot, self.k_total, out=self.y_slots,
                            workspace=self.ffn_ws)

@@ -1,9 +1,11 @@
 // Weighted combine (Cascadia, Sec. 3.1 "weighted reduction"; FP32 output as in Cascadia Fig. 2):
 //   y[t, :] = sum_{j ascending} weights[t, j] * y_slots[t*k + j, :]
+// A slot of weight 0 adds nothing, whatever its row holds: the expert FFN does not write the rows of empty slots, and
+// 0 times what stands there may be NaN.
 // One thread owns four consecutive outputs of one token (16-byte loads and stores); no atomics.
 // The slots are read in batches of kBatch with all of a batch's loads issued before the first
 // multiply-add (a load-then-use loop waits one memory latency per slot); indices past the last
-// slot re-read the last one (a cache hit) and their products are dropped.
+// slot re-read the last one (a cache hit) and their products are dropped, as those of weight 0 are.
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -33,7 +35,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {  // selects, not a branch: the loads stay ahead of the adds
-      const bool ok = j0 + u < k_total;
+      const bool ok = j0 + u < k_total && w[u] != 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float s = acc[e] + w[u] * v[u][e];
@@ -68,6 +70,7 @@ __global__ __launch_bounds__(256) void combine_restore_kernel(const uint16_t* __
     const float w = wt[j] * rF;
     const u32x2 v = *reinterpret_cast<const u32x2*>(src + (int64_t)j * H);
     const f16x2 a = bitcast<f16x2>(v[0]), b = bitcast<f16x2>(v[1]);
+    if (wt[j] == 0.0f) continue;
     acc[0] += w * (float)a[0];
     acc[1] += w * (float)a[1];
     acc[2] += w * (float)b[0];

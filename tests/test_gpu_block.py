@@ -182,3 +182,68 @@ def test_masked_experts_leave_slots_empty():
     ids = block.ids.cpu().numpy()
     assert set(np.unique(ids[:, :4])) <= {-1, 2, 9, 30} and np.all((ids[:, :4] == -1).sum(1) >= 1)
     assert np.all(block.weights.cpu().numpy()[ids == -1] == 0) and bool(torch.isfinite(y).all())
+
+
+@pytest.mark.parametrize("mx", [None, "fp8"])
+def test_slots_that_logits_leave_empty(mx):
+    """Logits of -inf leave a token with fewer experts than slots, or none: choice, buckets, FFN and combine give
+    what its experts alone give, whatever the slots' rows hold."""
+    T, kt = 9, 4
+    L, block, *_ = make(T, mx)
+    W, x = block.W, torch.randn(T, 512, device=DEV).bfloat16()
+    logits = torch.randn(T, 32, device=DEV)
+    logits[1, 3:] = -float("inf")
+    logits[4] = -float("inf")
+    logits[7, 1:] = float("nan")
+    ids, w, _ = moe.moe_select_experts(logits, moe.RouteRule(kt, "sigmoid"))
+    b = moe.moe_bucket(ids, W.n_experts)
+
+    def ffn(fill):
+        ys = torch.full((T * kt, 512), fill, device=DEV)
+        if mx:
+            moe.moe_expert_ffn_mx(x, W, mx, b.offsets, b.sorted_slot, kt, out=ys)
+        else:
+            moe.moe_expert_ffn(x, W, b.offsets, b.sorted_slot, kt, out=ys)
+        return ys
+
+    want = moe.moe_combine(ffn(0.0), w)
+    assert (ids == -1).sum(1).tolist() == [0, 1, 0, 0, 4, 0, 0, 3, 0] and not bool(want[4].any())
+    assert bool(torch.isfinite(want).all()) and bool(want[[1, 7]].any(1).all())
+    for fill in (float("nan"), float("inf"), -3.0):
+        assert torch.equal(moe.moe_combine(ffn(fill), w), want)
+
+
+def test_empty_slots_in_restored_sums():
+    """moe_combine_restore, likewise: a slot of weight 0 adds nothing, whatever its row holds."""
+    T, kt, H = 3, 4, 64
+    g = torch.Generator().manual_seed(3)
+    ys = torch.randn(T * kt, H, generator=g).half().to(DEV)
+    w = torch.rand(T, kt, generator=g).to(DEV)
+    w[0, 2] = w[1, :] = 0.0
+    rows = torch.tensor([2, 4, 5, 6, 7], device=DEV)
+    ys[rows] = 0.0
+    want = moe.moe_combine_restore(ys, w, 2)
+    for fill in (float("nan"), float("inf")):
+        ys[rows] = fill
+        assert torch.equal(moe.moe_combine_restore(ys, w, 2), want)
+
+
+def test_a_token_that_is_not_finite_depends_on_no_earlier_pass():
+    """A token of NaN has no expert to go to: its output is the same after any earlier pass, and no other token's
+    output changes."""
+    T = 6
+    L, block, attn, res, *_ = make(T)
+    y0, _ = block.forward(attn, res)
+    y0 = y0.clone()
+    bad = res.clone()
+    bad[2, 5] = float("nan")
+    seen = []
+    for fill in (0.0, float("nan"), 7.0):
+        block.y_slots.fill_(fill)
+        y, r = block.forward(attn, bad)
+        assert (block.ids[2, :4] == -1).all() and bool(torch.isnan(r[2, 5]))
+        seen.append(y.clone())
+    keep = [0, 1, 3, 4, 5]
+    for y in seen:
+        assert torch.equal(y[keep], y0[keep])
+        assert torch.equal(y[2].view(torch.int32), seen[0][2].view(torch.int32))
