@@ -17,6 +17,8 @@
 // VPL consecutive experts of its group, so the lanes hold the experts in ascending order (which makes "the
 // lowest lane, then the lowest register" the lowest index) and a group is reduced by butterflies inside its
 // lanes.  Vector instructions bound it, not bytes.
+#include <cfloat>
+
 #include "launch.hpp"
 #include "values.hpp"
 
@@ -305,7 +307,7 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelArgs a) {
     for (int v = 0; v < VPL; ++v)
       merge2(m1, m2, (a.group_max && !a.bias && key[v] != -INFINITY) ? L[v] : key[v], -INFINITY);
     merge_group(m1, m2, a.lanes);
-    const bool one = a.group_max || m2 == -INFINITY;
+    const bool one = a.group_max || m2 == -INFINITY, any = m1 != -INFINITY;  // any: an expert is available
     const float rank = one ? m1 : m1 + m2;
     int before = 0;
     for (int g = 0; g < a.n_groups; ++g) {
@@ -314,10 +316,11 @@ __global__ __launch_bounds__(64 * kSelWaves) void select_kernel(SelArgs a) {
     }
     keep = before < a.topk_groups;
     if (!(a.group_max && !a.bias)) {  // (the largest logit as the rank is exact)
-      // distance of the rank from its exact value: two scores, two roundings of a key, one of the sum
+      // distance of the rank from its exact value: two scores, two roundings of a key, one of the sum; infinite
+      // where two finite keys sum beyond fp32, which leads to 64 bits whatever the other ranks are
       const float rerr = 2.0f * err + 2.0f * kEps * (fabsf(m1) + (one ? 0.0f : fabsf(m2)));
-      const float lo = -wave_max_f32(keep && rank != -INFINITY ? rerr - rank : -INFINITY);
-      const float hi = wave_max_f32(!keep && rank != -INFINITY ? rerr + rank : -INFINITY);
+      const float lo = -wave_max_f32(keep && any ? rerr - fminf(rank, FLT_MAX) : -INFINITY);
+      const float hi = wave_max_f32(!keep && any ? rerr + fmaxf(rank, -FLT_MAX) : -INFINITY);
       if (hi >= lo) {  // uniform; the ranks again, in 64 bits
         double x[VPL], sum = 0.0, d1 = -INFINITY, d2 = -INFINITY;
 #pragma unroll

@@ -259,3 +259,24 @@ def test_matches_the_plain_routers():
 def test_empty_batch():
     ids, w, s = moe.moe_select_experts(torch.empty(0, 16, device=DEV), moe.RouteRule(2), want_scores=True)
     assert ids.shape == (0, 2) and s.shape == (0, 16)
+
+
+def test_ranks_past_fp32():
+    """Finite biases near the end of fp32: two of them overflow as a group's rank, which stays a rank (a group with
+    available experts comes before one without, and a larger sum before a smaller)."""
+    low = float(torch.finfo(torch.float32).min)
+    E = 32
+    groups = [  # a bias per group of eight
+        (-float("inf"), -2e38, -3e38, 0.1), (-float("inf"), low, low, 0.1), (-float("inf"), low, -float("inf"), low),
+        (-3e38, -2e38, -float("inf"), low), (1.9e38, 2e38, -low, 0.0), (2e38, 2e38, 1.9e38, -low), (-low, -low, -low, 1.0),
+        (1e38, -float("inf"), low, -2e38)]
+    for score in ("softmax", "sigmoid"):
+        for per_group in groups:
+            bias = torch.tensor(per_group).repeat_interleave(8)
+            for keep in (1, 2, 3):
+                for by in ("top2", "max"):
+                    check(logits(3, E, seed=7), top_k=6, score=score, bias=bias, n_groups=4, topk_groups=keep,
+                          group_score=by)
+        mixed = torch.tensor([2e38, -2e38] + [low] * 6).repeat(4)  # the sum of a group's two is small
+        mixed[8] = 2.1e38
+        check(logits(3, E, seed=7), top_k=6, score=score, bias=mixed, n_groups=4, topk_groups=2)
