@@ -172,8 +172,11 @@ moe_status moe_route_sigmoid(const void *x, moe_act_dtype x_dtype, int T, int H,
  *             weights of 0;
  *   shared    slots top_k .. top_k+n_shared-1 hold experts E .. E+n_shared-1 with weight shared_weight.
  * The choice is that of the keys in 64 bits, also where two keys or ranks are closer than fp32 can
- * tell.  It is a function of the logits; ids of moe_route_grouped also depend on the logits' own fp32
- * rounding, as moe_route's do.
+ * tell.  Without a bias the logits stand for the keys (in a group's MAX rank too): the scores rise with
+ * them, also where 64 bits cannot tell the scores apart (SIGMOID of logits beyond 37, SOFTMAX 745 below
+ * the largest).  With a bias, a bias of zeros among them, such keys tie and the lowest index comes
+ * first; so do TOP2 ranks, which are sums of scores.  The choice is a function of the logits; ids of
+ * moe_route_grouped also depend on the logits' own fp32 rounding, as moe_route's do.
  * The struct is a HOST struct; selection_bias is a device pointer to [E] fp32, or NULL. */
 #define MOE_MAX_GROUPS 64
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;

@@ -280,3 +280,21 @@ def test_ranks_past_fp32():
         mixed = torch.tensor([2e38, -2e38] + [low] * 6).repeat(4)  # the sum of a group's two is small
         mixed[8] = 2.1e38
         check(logits(3, E, seed=7), top_k=6, score=score, bias=mixed, n_groups=4, topk_groups=2)
+
+
+def test_scores_that_64_bits_cannot_tell_apart():
+    """Sigmoid scores of logits beyond 37 are all 1 in 64 bits, softmax scores 745 below the largest all 0.  Without
+    a bias the logits order such experts; keys with a bias tie, so the lowest index comes first."""
+    L = torch.linspace(40.0, 60.0, 64).repeat(2, 1)
+    zero = torch.zeros(64, device=DEV)
+    ids = lambda X, **k: moe.moe_select_experts(X.to(DEV), moe.RouteRule(6, **k))[0].cpu().tolist()[0]
+    assert ids(L, score="sigmoid") == [63, 62, 61, 60, 59, 58]
+    assert ids(L, score="sigmoid", selection_bias=zero) == [0, 1, 2, 3, 4, 5]
+    grouped = dict(score="sigmoid", n_groups=4, topk_groups=1)
+    assert ids(L, group_score="max", **grouped) == [63, 62, 61, 60, 59, 58]
+    assert ids(L, group_score="top2", **grouped) == [15, 14, 13, 12, 11, 10]  # (ranks are sums of scores: they tie)
+    assert ids(L, group_score="max", selection_bias=zero, **grouped) == [0, 1, 2, 3, 4, 5]
+    L = torch.linspace(-900.0, -800.0, 64).repeat(2, 1)
+    L[:, 20] = 0.0
+    assert ids(L) == [20, 63, 62, 61, 60, 59]
+    assert ids(L, selection_bias=zero) == [20, 0, 1, 2, 3, 4]
