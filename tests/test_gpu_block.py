@@ -247,3 +247,25 @@ def test_a_token_that_is_not_finite_depends_on_no_earlier_pass():
     for y in seen:
         assert torch.equal(y[keep], y0[keep])
         assert torch.equal(y[2].view(torch.int32), seen[0][2].view(torch.int32))
+
+
+def test_the_next_block_adds_the_output():
+    """Two blocks in turn, in place: the second block's residual is the first one's plus its output, and what it
+    routes is the norm of that sum."""
+    a, b = make(9), make(9, seed=5)
+    y1, r = a[1].forward(a[2], a[3], a[3])
+    before, y1 = r.clone(), y1.clone()
+    b[1].W_o = None
+    y2, r2 = b[1].forward(y1, r, r)
+    torch.cuda.synchronize()
+    f = lambda v: v.double().cpu().numpy()
+    s, x = ref.add_rms_norm(f(y1), f(before), b[5], 1e-6)
+    rel = (512 / 256 + 80) * 2.0 ** -24  # as derived for the norm: its fp32 steps
+    assert np.all(np.abs(f(r2) - s) <= np.abs(s) * (2.0 ** -8 + 2.0 ** -23))
+    assert np.all(np.abs(f(b[1].x) - x) <= np.abs(x) * (2.0 ** -8 + 2 * rel))
+    orc, block = oracle.load(), b[1]
+    bk = orc.bucket(block.ids.cpu().numpy(), b[0].wl.n_experts)
+    xb = block.x.view(torch.int16).cpu().numpy().view(np.uint16)
+    ys = orc.expert_ffn(xb, oracle.X_BF16, block.k_total, oracle.ExpertWeights.from_layer(b[0]), bk["offsets"],
+                        bk["sorted_slot"])
+    assert rms_ratio(f(y2), orc.combine(ys, block.weights.cpu().numpy())) <= EXACT_TOL
