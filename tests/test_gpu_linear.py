@@ -235,3 +235,19 @@ def test_int4_codes_at_their_zero_point(T, N, K):
     got = moe.moe_linear(x.to(DEV), W).double().cpu().numpy()
     bad = ~(np.abs(got - want) <= ref.linear_tolerance(xs, w, K, want, "fp32"))
     assert not bad.any(), (int(bad.sum()), got[bad][:4], want[bad][:4])
+
+
+@pytest.mark.parametrize("e", [0, 1, 2, 8, 29])
+@pytest.mark.parametrize("T,N,K", [(1, 32, 128), (4, 40, 288), (20, 33, 128), (150, 32, 128), (1025, 1000, 96)])
+def test_smallest_scale_codes(T, N, K, e):
+    """MXFP4 scale codes from 2^-127 on, whose weights are bf16 subnormals, with x large enough for normal sums."""
+    rng = np.random.default_rng(e)
+    codes, _, _, _, _ = ref.weights("mxfp4", N, K, rng)
+    c = np.stack([codes & 15, codes >> 4], 2).reshape(N, K)
+    scales = np.full((N, K // 32), e, np.uint8)
+    w = ref.E2M1[c] * 2.0 ** (e - 127.0)
+    X = torch.from_numpy(rng.standard_normal((T, K)) * 2.0 ** 100).bfloat16()
+    x = X.double().numpy()
+    want = x @ w.T
+    got = moe.moe_linear(X.to(DEV), moe.LinearWeights(dev(codes), dev(scales))).double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= ref.linear_tolerance(x, w, K, want, "fp32"))
