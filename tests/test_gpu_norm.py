@@ -160,3 +160,21 @@ def test_other_stream_and_repeat():
     torch.cuda.synchronize()
     for u, v in zip(a, b):
         assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("H", [256, 263, 4096, 5])
+def test_rows_that_are_not_finite_stay_alone(H):
+    """A NaN makes its row NaN; an infinity gives NaN where it stands and 0 beside it (its mean square is infinite);
+    the other rows do not change."""
+    T = 6
+    X = torch.randn(T, H, device=DEV)
+    R = torch.randn(T, H, device=DEV).bfloat16()
+    norm = moe.RmsNorm(torch.rand(H, device=DEV) + 0.5)
+    a = moe.moe_add_rms_norm(X, norm, R)
+    X2 = X.clone()
+    X2[1, H - 1], X2[4, 2] = float("nan"), float("inf")
+    b = moe.moe_add_rms_norm(X2, norm, R)
+    keep = [0, 2, 3, 5]
+    assert torch.equal(a[0][keep], b[0][keep]) and torch.equal(a[1][keep], b[1][keep])
+    assert bool(torch.isnan(b[0][1]).all()) and torch.isnan(b[0][4]).nonzero().flatten().tolist() == [2]
+    assert int(torch.count_nonzero(b[0][4])) == 1 and bool(torch.isinf(b[1][4, 2])) and bool(torch.isnan(b[1][1, H - 1]))
