@@ -671,9 +671,25 @@ void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
   else linear_dot_kernel<FMT, TT, 4><<<g, 256, 0, stream>>>(a);
 }
 
-// Rows (16 rt) and tokens (16 mt) of a streaming workgroup: the fewest that leave at most one workgroup per CU, since
-// those of a second round start when the first have ended (32 tokens x 4096 MXFP4: 4096 rows 8.0 us, 4500 rows 13.8
-// with 16 rows a workgroup and 9.5 with 32; 8192 rows 10.2 with 32, 8838 rows 16.9, and 13.4 with 64).  More than 32
+// Rows (16 rt) and tokens (16 mt) of a streaming workgroup.
+// Up to 16 tokens two workgroups of 16 or 32 rows share a CU (53 and 74 KB of LDS), one of 64 has it alone.  16 rows
+// while each workgroup has a CU of its own (INT4, whose decoding bounds it: to 12288 rows), 32 beyond; MXFP4 from six
+// spans of K on takes 64 where they leave the last round of the card more than half full.  us for 16 tokens with 16, 32
+// and 64 rows a workgroup:
+//   MXFP4  K = 1024   8300 rows  6.1  4.9  5.8    NVFP4  K = 4096   4096 rows  6.2  7.6 11.3
+//          K = 1536  16384       9.0  6.9  6.7                      6144       9.2  8.1 11.6
+//          K = 4096   4096       6.2  7.0  9.8                     12800      16.0 12.7 12.6
+//                     6144       9.0  7.3 10.1                     18432      19.0 17.1 22.2
+//                     8300      11.8 11.2 10.5                     32768      29.8 24.0 25.2
+//                    16384      16.0 12.7 12.6    INT4   K = 1024   9216       7.9  6.8  9.3
+//                    18432      18.5 16.5 19.5           K = 4096   6144      10.7 10.9 17.1
+//          K = 7168   8300      18.3 17.7 15.8                     12288      15.2 16.7 18.1
+//                    18432      29.8 26.5 30.1                     12800      18.3 16.8 18.4
+//                    32768      47.3 37.9 35.3                     18432      22.5 23.0 32.8
+//                   129280     173.4 133.0 127.1         K = 7168   9216      23.0 25.6 29.5
+// Beyond 16 tokens a workgroup has a CU alone: the fewest rows that leave at most one workgroup per CU, since those of
+// a second round start when the first have ended (32 tokens x 4096 MXFP4: 4096 rows 8.0 us, 4500 rows 13.8 with 16
+// rows a workgroup and 9.5 with 32; 8192 rows 10.2 with 32, 8838 rows 16.9, and 13.4 with 64).  More than 32
 // tokens take a workgroup per 32 or 64 of them and rows, in place of tiles (mt 0), while one round holds them all and
 // K is not long, since then a tile's steps and the join of its shares wait for their loads (us, streamed and tiles:
 // 135 x 257 x 1728 INT4 5.6 and 15.1, 256 x 1024 x 2048 MXFP4 7.0 and 11.6, 128 x 4096 x 4096 13.3 and 18.9, 512 x
@@ -685,7 +701,11 @@ struct StreamPlan {
   int rt, mt;
 };
 StreamPlan stream_plan(int fmt, int T, int N, int K) {
-  if (T <= 16) return {N <= 16 * kCus ? 1 : N <= 32 * kCus ? 2 : 4, 1};
+  if (T <= 16) {
+    if (N <= (fmt == MOE_W_INT4_G32 ? 48 : 16) * kCus) return {1, 1};
+    const int last = (N + 63) / 64 % kCus;  // 64-row workgroups of the last round, 0: it is full
+    return {fmt == MOE_W_MXFP4 && K > 5 * kSpan && (last == 0 || last > kCus / 2) ? 4 : 2, 1};
+  }
   if (T > 32 && K > 12288) return {0, 0};
   constexpr StreamPlan sizes[] = {{1, 2}, {2, 2}, {4, 2}, {4, 4}};
   for (const StreamPlan& p : sizes) {

@@ -251,3 +251,11 @@ def test_smallest_scale_codes(T, N, K, e):
     want = x @ w.T
     got = moe.moe_linear(X.to(DEV), moe.LinearWeights(dev(codes), dev(scales))).double().cpu().numpy()
     assert np.all(np.abs(got - want) <= ref.linear_tolerance(x, w, K, want, "fp32"))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,N,K", [(16, 4097, 288), (5, 12288, 96), (9, 12289, 96), (16, 8192, 1312), (12, 8193, 1280),
+                                   (7, 8193, 1312), (16, 16384, 1312), (6, 16385, 1312), (13, 24640, 1312)])
+def test_rows_of_a_workgroup(fmt, T, N, K):
+    """Up to 16 tokens on both sides of every change of the workgroups' rows."""
+    check(T, N, K, fmt, "bf16")
