@@ -269,3 +269,20 @@ def test_the_next_block_adds_the_output():
     ys = orc.expert_ffn(xb, oracle.X_BF16, block.k_total, oracle.ExpertWeights.from_layer(b[0]), bk["offsets"],
                         bk["sorted_slot"])
     assert rms_ratio(f(y2), orc.combine(ys, block.weights.cpu().numpy())) <= EXACT_TOL
+
+
+@pytest.mark.parametrize("mx", [None, "fp8"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_no_token_has_an_expert(T, mx):
+    """Every slot empty: the FFN has no row to compute, and the combine gives zeros."""
+    W = make(1, mx)[1].W
+    x = torch.randn(T, 512, device=DEV).bfloat16()
+    ids, w, _ = moe.moe_select_experts(torch.full((T, 32), -float("inf"), device=DEV), moe.RouteRule(4))
+    b = moe.moe_bucket(ids, W.n_experts)
+    ys = torch.full((T * 4, 512), float("nan"), device=DEV)
+    if mx:
+        moe.moe_expert_ffn_mx(x, W, mx, b.offsets, b.sorted_slot, 4, out=ys)
+    else:
+        moe.moe_expert_ffn(x, W, b.offsets, b.sorted_slot, 4, out=ys)
+    y = moe.moe_combine(ys, w)
+    assert bool((ids == -1).all()) and not bool(y.any())
