@@ -443,7 +443,10 @@ moe_status moe_expert_ffn_mx_codes(const uint8_t *x_codes, const uint8_t *x_scal
  *   residual_out[t,:] = s
  *   y[t,h] = s[h] * weight[h] / sqrt(sum_h s[h]^2 / hidden + eps)
  *   codes[t], scales[t] = the MX block quantisation (see MX mode) of the fp32 y before it is rounded to y_dtype;
- *   fmt MOE_MX_FP8_E4M3 is the 8-bit output, in the layout of moe_expert_ffn_mx_codes.  y must be finite there.
+ *   fmt MOE_MX_FP8_E4M3 is the 8-bit output, in the layout of moe_expert_ffn_mx_codes.  y must be finite there (the
+ *   codes hold no NaN: one becomes a finite value).
+ * A NaN in s makes its row's y NaN, an infinity NaN where it stands and 0 elsewhere, as does a sum of squares past
+ * fp32 (0 everywhere); other rows are untouched.
  * Types: x, residual (and residual_out), weight and y each bf16, fp16 or fp32.  x may be moe_combine's or
  * moe_linear's fp32 output, y is what moe_route, moe_linear and moe_expert_ffn read.
  *   x, residual, residual_out  [T] rows of `hidden` values, *_row_stride values apart (>= hidden), aligned to a
@@ -475,6 +478,9 @@ moe_status moe_add_rms_norm(const moe_norm *norm, const void *x, moe_dtype x_dty
  *   bias [n_out] fp32, or NULL
  *   y    [T] rows of n_out values (bf16, fp16 or fp32), y_row_stride values apart (>= n_out), aligned to a value
  *   workspace moe_linear_workspace_bytes(T, W) bytes, 16-byte aligned (NULL if that is 0)
+ * Up to four tokens sum a block's products before its scale is applied, which stays inside fp32 while |x| <
+ * 2^119.  A NaN or infinity in x makes that token's outputs NaN or infinite and no other token's (INT4 weights may
+ * make an infinity NaN: they multiply in two parts).
  * Errors: NULL, SHAPE (also a weight, scale or zero-point row stride of 2^24 bytes or more, an x row stride of
  * 2^23 values or more, T > 2^30, or n_out > 2^26), BLOCK, ALIGN, DTYPE (FP16 weights, x not bf16), WORKSPACE, HIP. */
 typedef struct {

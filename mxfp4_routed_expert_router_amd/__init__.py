@@ -845,15 +845,15 @@ class MoELayer:
 
 
 class MoEBlock:
-    """The MoE half of a decoder block, every buffer allocated once for T tokens so that forward() only enqueues
-    library calls (capturable in a HIP graph): the attention output's projection (4-bit weights; left out
+    """The MoE half of a decoder block, its buffers allocated once for T tokens so that forward() only enqueues
+    library calls (capturable in a HIP graph; a call that is given no residual_out allocates one): the attention output's projection (4-bit weights; left out
     without W_o), the residual addition and norm, routing by a rule, bucketing, the expert FFN and the combine.
     With mx ("fp8", "fp6", "fp4") the norm writes the MX codes that the expert FFN reads.
 
     forward(attn, residual) -> (y fp32 [T][H], residual_out): the next block's norm adds y to residual_out.
 
     Slots that a bias or logits that are not finite leave empty add nothing; a token none of whose logits is finite
-    (NaN in its row) gets its shared experts alone.  Passes of one block share its buffers, so they run one after
+    (NaN in its row, which residual_out shows) gets its shared experts alone, whose MX codes hold no NaN.  Passes of one block share its buffers, so they run one after
     another on one stream."""
 
     def __init__(self, W: ExpertWeights, T: int, rule: RouteRule, w_router: torch.Tensor, norm: RmsNorm,

@@ -279,7 +279,7 @@ __global__ __launch_bounds__(64 * NW) void linear_dot_kernel(LinArgs a) {
 // (earlier, or two spans ahead: the same or slower).  No load is conditional (registers of loads in flight would be
 // merged, and waited for, at the end of each turn): lanes past K and past the wave's share read zeros.
 // Bound: not by bandwidth (32 tokens, 16384 rows x 4096 NVFP4: 39 MB in 17 us, 2.3 TB/s; 16 tokens, 7168 x 7168
-// MXFP4: 27 MB in 11.2 us).  Reading the weights (5.5 us of the 17), all of x once per workgroup through the L2,
+// MXFP4: 27 MB in 11.5 us).  Reading the weights (5.5 us of the 17), all of x once per workgroup through the L2,
 // both through LDS, and decoding follow one another in each wave, and the registers leave two waves per SIMD.
 template <int FMT, int RT, int MT, int NW>
 __global__ __launch_bounds__(64 * NW) void linear_stream_kernel(LinArgs a) {
@@ -662,7 +662,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinArgs a, int splits)
 }
 
 // Eight rows per workgroup; eight waves where the rows give at most a workgroup per CU (one token, 1000 x 2080
-// INT4 3.2 against 3.3 us with four waves, 512 x 7168 NVFP4 4.2 against 5.5), four beyond (7168 x 7168 MXFP4 7.9
+// INT4 3.3 against 3.5 us with four waves, 512 x 7168 NVFP4 3.5 against 4.3), four beyond (7168 x 7168 MXFP4 7.9
 // against 9.2).
 template <int FMT, int TT>
 void launch_dot_tokens(const LinArgs& a, hipStream_t stream) {
@@ -722,9 +722,9 @@ void launch_stream(const LinArgs& a, hipStream_t stream) {
   linear_stream_kernel<FMT, RT, MT, NW><<<g, 64 * NW, 0, stream>>>(a);
 }
 
-// Three and four tokens: dot products up to this many rows, where the streaming kernel has fewer than 200 workgroups
-// (4 tokens, 2048 x 7168 MXFP4: 6.1 us, streamed 7.5; 4096 x 4096: 5.9 and 5.6; 7168 x 7168: 13.7 and 10.2).  Two
-// tokens are faster by dot products at every size (7168 x 7168 MXFP4 9.1 us and 9.8, INT4 13.0 and 17.3).
+// Three and four tokens: dot products up to this many rows, 200 workgroups of the streaming kernel (4 tokens, 2048 x
+// 7168 MXFP4: 6.0 us, streamed 7.5; 4096 x 4096: 5.9 and 5.6; 7168 x 7168: 13.7 and 10.2; 3200 x 4096 INT4 6.7 and
+// 7.0).  Two tokens are faster by dot products at every size (7168 x 7168 MXFP4 9.1 us and 9.8, INT4 13.0 and 17.7).
 constexpr int kDotRows = 16 * 200;
 
 // Tiles and K shares of the tile kernel.  128-token tiles where they give a workgroup per CU (2048 tokens x 4096 x
