@@ -494,6 +494,107 @@ moe_status moe_linear(const void *x, moe_act_dtype x_dtype, int64_t x_row_stride
                       int64_t y_row_stride, void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * Attention: the other half of the block (not on the pages).  The projected q, k and v turn by their positions and go
+ * into a paged cache (moe_rope_cache); a prompt attends over its own rows (moe_attention_prompt), a new token over the
+ * cache (moe_attention_decode).  Query heads h = 0 .. n_q_heads-1 share key-value heads in groups of
+ * G = n_q_heads / n_kv_heads: h reads key-value head h / G.
+ *
+ * moe_heads: [tokens][heads][head_dim] values; a head's values are contiguous, tokens and heads are token_stride and
+ * head_stride values apart (both >= 0), so that q, k and v may be parts of one product's output.  A HOST struct. */
+#define MOE_MAX_HEADS 1024
+#define MOE_MAX_HEAD_DIM 256   /* a multiple of 8 */
+typedef struct {
+  void *p;                     /* inputs are read only */
+  moe_dtype dtype;
+  int64_t token_stride, head_stride;
+} moe_heads;
+
+/* A key-value cache of n_pages pages of page_size tokens each: value d of token i of page p and key-value head h is
+ * value p * page_stride + h * head_stride + i * token_stride + d of k or v (any order of the three; 64-bit offsets).
+ * Formats: MOE_KV_BF16 and MOE_KV_FP16 hold the values; MOE_KV_MXFP8 holds MOE_MX_FP8_E4M3 codes (one byte each) with an
+ * E8M0 scale byte per 32 values along head_dim at s_page_stride, s_head_stride, s_token_stride (scales NULL otherwise;
+ * head_dim % 32 == 0, else MOE_ERR_BLOCK).  k, v: 16-byte aligned, strides multiples of 16 bytes.
+ * n_pages * page_size < 2^31.  A HOST struct. */
+typedef enum { MOE_KV_BF16 = 0, MOE_KV_FP16 = 1, MOE_KV_MXFP8 = 2 } moe_kv_format;
+typedef struct {
+  moe_kv_format fmt;
+  int n_pages, page_size, n_kv_heads, head_dim;
+  void *k, *v;
+  int64_t page_stride, head_stride, token_stride;
+  uint8_t *k_scales, *v_scales;
+  int64_t s_page_stride, s_head_stride, s_token_stride;
+} moe_kv_cache;
+
+/* Angles of the positions: cos and sin [n_positions][rotary_dim / 2] fp32.  Of a head's first rotary_dim values (even,
+ * at most head_dim) pair i is (i, i + rotary_dim/2) (HALVES) or (2i, 2i + 1) (NEIGHBOURS); the others stay. */
+typedef enum { MOE_ROPE_HALVES = 0, MOE_ROPE_NEIGHBOURS = 1 } moe_rope_pairs;
+typedef struct {
+  const float *cos, *sin;
+  int n_positions, rotary_dim;
+  moe_rope_pairs pairs;
+} moe_rope;
+
+/* moe_rope_cache -- per token t, in fp32 with one rounding at each output: pairs (a, b) of q's and k's heads become
+ * (a cos - b sin, b cos + a sin) at position positions[t]; q_out, k_out and v_out (bf16, fp16 or fp32) get the turned q
+ * and k, and v; slot slots[t] = page * page_size + token of the cache gets the turned k, and v (MXFP8: codes of the fp32
+ * values, which must be finite).
+ *   rope, positions  [T] int32, or both NULL (nothing turns).  A token whose position is outside [0, n_positions) is
+ *                    padding: none of its outputs is written
+ *   q, k, v          bf16, fp16 or fp32, the same for all, aligned to a value.  n_q_heads or n_kv_heads may be 0 (then
+ *                    those pointers are not used); v may be NULL where neither v_out nor cache is given
+ *   q_out            may be q itself (same pointer, type and strides: it turns in place); so may k_out and v_out
+ *   k_out, v_out     or NULL
+ *   cache, slots     [T] int32, or both NULL.  A slot outside the cache is not written.  Slots that two tokens of a call
+ *                    share hold a mixture of both
+ * Errors: NULL (also key-value heads without any output), SHAPE (T<0, T * (n_q_heads + 2 n_kv_heads) > 2^27, heads,
+ * head_dim, strides, rotary_dim, a cache of other heads, in place with other strides), BLOCK, DTYPE, ALIGN, HIP. */
+moe_status moe_rope_cache(const moe_rope *rope, const int32_t *positions, int T, int n_q_heads, int n_kv_heads,
+                          int head_dim, const moe_heads *q, const moe_heads *k, const moe_heads *v,
+                          const moe_heads *q_out, const moe_heads *k_out, const moe_heads *v_out,
+                          const moe_kv_cache *cache, const int32_t *slots, void *stream);
+
+/* moe_attention_prompt -- n_seqs sequences packed one after another: sequence b has queries cu_q[b] .. cu_q[b+1]-1 and
+ * keys cu_k[b] .. cu_k[b+1]-1 (device int32 [n_seqs+1], ascending; clamped to [0, Tq] and [0, Tk]).  With nq queries and
+ * nk keys, query i stands at key position p = i + nk - nq and sees keys j with j <= p (causal) and j > p - window
+ * (window > 0; causal only):
+ *   y[i,h] = sum_j softmax_j(scale * q[i,h] . k[j,h/G]) v[j,h/G],  lse[i,h] = ln sum_j exp(scale * q[i,h] . k[j,h/G])
+ * (fp32 sums; the exponentials are rounded to the 16-bit type before their product with v; one rounding of y).  A row
+ * that sees no key, or only keys of score -inf, gets y = 0 and lse = -inf.  A NaN or infinity in a key or value reaches
+ * the rows that see it and no other.  Rows of y outside the sequences are not touched.
+ *   q, y  [Tq][n_q_heads][head_dim], k, v [Tk][n_kv_heads][head_dim]: one type, bf16 or fp16; 16-byte aligned, strides
+ *         multiples of 8 values
+ *   lse   [Tq][n_q_heads] fp32, or NULL
+ *   workspace moe_attention_prompt_workspace_bytes(...) bytes, 16-byte aligned (NULL if that is 0)
+ * Errors: NULL, SHAPE (Tq<0, Tk<0, n_seqs<0 or >2^20, heads, head_dim, Tq * n_q_heads or Tq + Tk from 2^31 on, more than
+ * 2^23 workgroups, a scale that is not positive and finite, window<0 or without causal), DTYPE, ALIGN, WORKSPACE, HIP. */
+size_t moe_attention_prompt_workspace_bytes(int Tq, int Tk, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim);
+moe_status moe_attention_prompt(const moe_heads *q, const moe_heads *k, const moe_heads *v, const int32_t *cu_q,
+                                const int32_t *cu_k, int n_seqs, int Tq, int Tk, int n_q_heads, int n_kv_heads,
+                                int head_dim, float scale, int causal, int window, const moe_heads *y, float *lse,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* moe_attention_decode -- row b is the newest token of a sequence with n = lens[b] cached tokens (its own among them;
+ * clamped to [0, max_len]), token j on page page_table[b][j / page_size] at j % page_size.  It sees the last `window` of
+ * them, or all (window 0):
+ *   y[b,h], lse[b,h] as for moe_attention_prompt (fp32 sums; the exponentials are two 16-bit parts, so an infinite
+ *   value that is seen may give NaN; one rounding of y).
+ * No keys: y = 0, lse = -inf.  Tokens on a page number outside [0, n_pages) are left out.  Rows may share pages and table
+ * rows (several newest tokens of one sequence: one row each, with rising lens).
+ *   q, y        [B][n_q_heads][head_dim] bf16 (MOE_KV_BF16, MOE_KV_MXFP8) or fp16 (MOE_KV_FP16), 16-byte aligned, strides
+ *               multiples of 8 values
+ *   page_table  [B] rows of table_width int32, table_stride apart;  lens [B] int32
+ *   max_len     at most table_width * page_size; the work is shared out by it, so it should be near the longest row
+ *   lse         [B][n_q_heads] fp32, or NULL
+ *   workspace   moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL if that is 0)
+ * Errors: NULL, SHAPE (B<0, B * n_q_heads > 2^23, heads, head_dim, strides, max_len, scale, window<0), BLOCK, DTYPE,
+ * ALIGN, WORKSPACE, HIP. */
+size_t moe_attention_decode_workspace_bytes(int B, int n_q_heads, int n_kv_heads, int head_dim, int max_len);
+moe_status moe_attention_decode(const moe_heads *q, int B, int n_q_heads, const moe_kv_cache *cache,
+                                const int32_t *page_table, int64_t table_stride, int table_width, const int32_t *lens,
+                                int max_len, float scale, int window, const moe_heads *y, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------------------------
  * moe_combine -- weighted reduction [C31] with FP32 output [C32]:
  *   y[t,:] = sum_{j = 0 .. k_total-1, in ascending j} weights[t,j] * y_slots[t*k_total+j,:]
  * Every output element has exactly one owner (no atomics).  A slot of weight 0 adds nothing, whatever

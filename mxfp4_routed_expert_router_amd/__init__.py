@@ -17,6 +17,12 @@ group-limited routing (MoEBlock runs them all):
     a = moe_linear(attn, W_o)                                          # 4-bit weights, fp32 out
     x, r, _, _ = moe_add_rms_norm(a, norm, residual)                   # residual stream and the layer's input
     ids, w, _ = moe_route_grouped(x, w_router, rule)                   # scores, bias, groups, top-k
+
+The attention that gives `attn` (AttentionBlock runs it with its norm and projection):
+
+    q, k, v = moe_rope_cache(q, k, v, rope, positions, cache, slots)   # rotary positions, write into the paged cache
+    attn, _ = moe_attention_prompt(q, k, v, cu)                        # whole prompts, packed
+    attn, _ = moe_attention_decode(q, cache, page_table, lens)         # one new token per sequence
 """
 from __future__ import annotations
 
@@ -41,6 +47,11 @@ DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # moe_dtype
 SCORES = {"softmax": 0, "sigmoid": 1}
 GROUP_SCORES = {"top2": 0, "max": 1}
 MOE_MAX_GROUPS = 64
+MOE_KV_BF16, MOE_KV_FP16, MOE_KV_MXFP8 = 0, 1, 2
+KV_FORMATS = {"bf16": MOE_KV_BF16, "fp16": MOE_KV_FP16, "mxfp8": MOE_KV_MXFP8}
+KV_TYPES = {MOE_KV_BF16: torch.bfloat16, MOE_KV_FP16: torch.float16, MOE_KV_MXFP8: torch.uint8}
+ROPE_PAIRS = {"halves": 0, "neighbours": 1}
+MOE_MAX_HEADS, MOE_MAX_HEAD_DIM = 1024, 256
 
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_BLOCK", 4: "MOE_ERR_ALIGN",
           5: "MOE_ERR_DTYPE", 6: "MOE_ERR_TOPK", 7: "MOE_ERR_WORKSPACE", 8: "MOE_ERR_HIP"}
@@ -79,6 +90,24 @@ class moe_norm(ctypes.Structure):
 
 class moe_linear_weights(ctypes.Structure):
     _fields_ = [("fmt", ctypes.c_int), ("n_out", ctypes.c_int), ("k_in", ctypes.c_int), ("w", moe_proj)]
+
+
+class moe_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("dtype", ctypes.c_int), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("s_page_stride", ctypes.c_int64),
+                ("s_head_stride", ctypes.c_int64), ("s_token_stride", ctypes.c_int64)]
+
+
+class moe_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("n_positions", ctypes.c_int),
+                ("rotary_dim", ctypes.c_int), ("pairs", ctypes.c_int)]
 
 
 _lib = None
@@ -155,6 +184,16 @@ def lib() -> ctypes.CDLL:
         L.moe_linear_workspace_bytes.restype = st; L.moe_linear_workspace_bytes.argtypes = [i, vp]
         L.moe_linear.restype = i
         L.moe_linear.argtypes = [vp, i, i64, i, vp, vp, vp, i, i64, vp, st, vp]
+        L.moe_rope_cache.restype = i
+        L.moe_rope_cache.argtypes = [vp, vp, i, i, i, i, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.moe_attention_prompt_workspace_bytes.restype = st
+        L.moe_attention_prompt_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.moe_attention_prompt.restype = i
+        L.moe_attention_prompt.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, ctypes.c_float, i, i, vp, vp, vp, st, vp]
+        L.moe_attention_decode_workspace_bytes.restype = st
+        L.moe_attention_decode_workspace_bytes.argtypes = [i, i, i, i, i]
+        L.moe_attention_decode.restype = i
+        L.moe_attention_decode.argtypes = [vp, i, i, vp, vp, i64, i, vp, i, ctypes.c_float, i, vp, vp, vp, st, vp]
         L.moe_stream_read.restype = i
         L.moe_stream_read.argtypes = [vp, st, vp, vp]
         _lib = L
@@ -787,6 +826,208 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
 
 
 # ----------------------------------------------------------------------------------------------------
+# Attention
+def _heads(what: str, t: torch.Tensor, shape, index: int) -> moe_heads:
+    """Description of a tensor [tokens][heads][head_dim] with contiguous heads on GPU `index` (-1: the CPU)."""
+    if t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{what} must be {tuple(shape)} on GPU {index}, got {tuple(t.shape)} on {t.device}")
+    ts, hs, ds = t.stride()
+    if ds != 1 and shape[2] > 1:
+        raise ValueError(f"{what}: a head's values must be contiguous, got strides {t.stride()}")
+    return moe_heads(t.data_ptr(), _dtype(what, t), ts if shape[0] > 1 else shape[1] * shape[2],
+                     hs if shape[1] > 1 else shape[2])
+
+
+def _ints(what: str, t: torch.Tensor, shape, index: int) -> int:
+    _dense(what, t, torch.int32, shape, index)
+    return t.data_ptr()
+
+
+class Rope:
+    """Cosines and sines of the positions' angles, fp32 [n_positions][rotary_dim / 2], and how values pair up
+    (moe_rope): "halves" (i, i + rotary_dim / 2) or "neighbours" (2i, 2i + 1)."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, pairs: str = "halves"):
+        _dense("Rope: cos", cos, torch.float32, cos.shape)
+        _dense("Rope: sin", sin, torch.float32, cos.shape)
+        if cos.dim() != 2 or cos.device != sin.device:
+            raise ValueError(f"Rope: cos and sin must be [n_positions][rotary_dim / 2] on one device, got "
+                             f"{tuple(cos.shape)} on {cos.device} and {sin.device}")
+        self.cos, self.sin, self.index = cos, sin, cos.get_device()
+        self.rotary_dim = 2 * cos.shape[1]
+        self.c = moe_rope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], self.rotary_dim, ROPE_PAIRS[pairs])
+        self.at = ctypes.addressof(self.c)
+
+
+class KvCache:
+    """A paged key-value cache (moe_kv_cache) on given tensors k and v [n_pages][n_kv_heads][page_size][head_dim], of
+    bf16, fp16 or (MXFP8) uint8 codes with scales uint8 [n_pages][n_kv_heads][page_size][head_dim / 32].  The last
+    dimension is contiguous, the others may be strided (a cache kept token by token is given as a permuted view); k and v
+    have the same strides.  KvCache.empty() allocates one, a head's tokens of a page next to each other."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
+        fmt = {t: f for f, t in KV_TYPES.items()}.get(k.dtype)
+        if fmt is None or v.dtype != k.dtype:
+            raise TypeError(f"KvCache: k and v must both be bfloat16, float16 or uint8, got {k.dtype} and {v.dtype}")
+        self.fmt, self.tensors, self.device, self.index = fmt, (k, v, k_scales, v_scales), k.device, k.get_device()
+
+        def strides(what, a, b, shape):
+            if a is None or b is None or a.shape != shape or b.shape != shape or a.device != k.device \
+                    or b.device != k.device or a.dtype != b.dtype:
+                raise ValueError(f"KvCache: {what} must be {tuple(shape)} on {k.device}")
+            sa, sb = a.stride(), b.stride()
+            if any(x != y for x, y, n in zip(sa, sb, shape) if n > 1) or (sa[3] != 1 and shape[3] > 1):
+                raise ValueError(f"KvCache: {what} must have the same strides and contiguous values, got {sa} and {sb}")
+            return [x if n > 1 else 0 for x, n in zip(sa[:3], shape)]
+
+        if k.dim() != 4:
+            raise ValueError(f"KvCache: k must be [n_pages][n_kv_heads][page_size][head_dim], got {tuple(k.shape)}")
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        page, head, token = strides("k and v", k, v, k.shape)
+        self.c = moe_kv_cache(fmt, self.n_pages, self.page_size, self.n_kv_heads, self.head_dim, k.data_ptr(),
+                              v.data_ptr(), page, head, token)
+        if fmt == MOE_KV_MXFP8:
+            if k_scales is None or k_scales.dtype != torch.uint8:
+                raise ValueError("KvCache: uint8 codes need uint8 scales")
+            page, head, token = strides("scales", k_scales, v_scales, k.shape[:3] + (self.head_dim // 32,))
+            self.c.k_scales, self.c.v_scales = k_scales.data_ptr(), v_scales.data_ptr()
+            self.c.s_page_stride, self.c.s_head_stride, self.c.s_token_stride = page, head, token
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("KvCache: 16-bit values take no scales")
+        self.act = torch.float16 if fmt == MOE_KV_FP16 else torch.bfloat16  # type of q and y
+        self.at = ctypes.addressof(self.c)
+        self._need = {}  # workspace bytes by (B, heads, max_len)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt: str = "bf16", device="cuda"):
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        make = lambda s, t: torch.empty(s, dtype=t, device=device)
+        t = KV_TYPES[KV_FORMATS[fmt]]
+        if fmt != "mxfp8":
+            return cls(make(shape, t), make(shape, t))
+        s = shape[:3] + (head_dim // 32,)
+        return cls(make(shape, t), make(shape, t), make(s, torch.uint8), make(s, torch.uint8))
+
+
+def moe_rope_cache(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor],
+                   rope: Optional[Rope] = None, positions: Optional[torch.Tensor] = None,
+                   cache: Optional[KvCache] = None, slots: Optional[torch.Tensor] = None, out=None):
+    """q [T][n_q_heads][head_dim], k and v [T][n_kv_heads][head_dim] (bf16, fp16 or fp32, one type, strided tokens and
+    heads) at int32 positions [T] -> (q, k, v) turned by the rope's angles (v as it is) in the cache's 16-bit type (bf16
+    without a cache); the turned k, and v, also go to int32 slots [T] (page * page_size + token) of the cache.  q may be
+    None, or k and v.  `out` gives the three buffers; a None there leaves that output out, and a buffer may be its input
+    itself."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("moe_rope_cache: needs q or k")
+    gpu = _gpu(x)
+    T, _, D = x.shape
+    nq = 0 if q is None else q.shape[1]
+    nkv = 0 if k is None else k.shape[1]
+    if out is None:
+        act = torch.bfloat16 if cache is None else cache.act
+        out = tuple(None if t is None else torch.empty((T, n, D), dtype=act, device=x.device)
+                    for t, n in ((q, nq), (k, nkv), (v if k is not None else None, nkv)))
+    described = [None if t is None else _heads(f"moe_rope_cache: {name}", t, (T, n, D), gpu)
+                 for name, t, n in (("q", q, nq), ("k", k, nkv), ("v", v, nkv), ("q_out", out[0], nq),
+                                    ("k_out", out[1], nkv), ("v_out", out[2], nkv))]
+    if rope is not None and rope.index != gpu or cache is not None and cache.index != gpu:
+        raise ValueError(f"moe_rope_cache: the rope and the cache must be on GPU {gpu}")
+    pos = None if positions is None else _ints("moe_rope_cache: positions", positions, (T,), gpu)
+    sl = None if slots is None else _ints("moe_rope_cache: slots", slots, (T,), gpu)
+    _enqueue("moe_rope_cache", gpu, None if rope is None else rope.at, pos, T, nq, nkv, D,
+             *(None if h is None else ctypes.addressof(h) for h in described), None if cache is None else cache.at, sl)
+    return out
+
+
+def moe_attention_prompt_workspace_bytes(Tq: int, Tk: int, n_seqs: int, n_q_heads: int, n_kv_heads: int,
+                                         head_dim: int) -> int:
+    return lib().moe_attention_prompt_workspace_bytes(Tq, Tk, n_seqs, n_q_heads, n_kv_heads, head_dim)
+
+
+def _attention_out(what: str, q: torch.Tensor, out, want_lse: bool, gpu: int):
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if want_lse else None)
+    y, lse = out
+    h = _heads(f"{what}: out", y, q.shape, gpu)
+    if lse is not None:
+        _dense(f"{what}: lse", lse, torch.float32, q.shape[:2], gpu)
+    return y, lse, h
+
+
+def moe_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor,
+                         cu_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+                         window: int = 0, want_lse: bool = False, out=None, workspace=None):
+    """Packed sequences: q [Tq][n_q_heads][head_dim], k and v [Tk][n_kv_heads][head_dim] (bf16 or fp16), sequence b's
+    rows cu_q[b] .. cu_q[b+1] and keys cu_k[b] .. cu_k[b+1] (int32 [n + 1]; cu_k None: cu_q) -> (y like q, lse fp32
+    [Tq][n_q_heads] or None).  scale None: head_dim ** -0.5.  Rows outside the sequences keep what `out` held."""
+    gpu = _gpu(q)
+    Tq, nq, D = q.shape
+    Tk, nkv = k.shape[:2]
+    n = cu_q.shape[0] - 1
+    qh = _heads("moe_attention_prompt: q", q, (Tq, nq, D), gpu)
+    kh = _heads("moe_attention_prompt: k", k, (Tk, nkv, D), gpu)
+    vh = _heads("moe_attention_prompt: v", v, (Tk, nkv, D), gpu)
+    y, lse, yh = _attention_out("moe_attention_prompt", q, out, want_lse, gpu)
+    cq = _ints("moe_attention_prompt: cu_q", cu_q, (n + 1,), gpu)
+    ck = cq if cu_k is None else _ints("moe_attention_prompt: cu_k", cu_k, (n + 1,), gpu)
+    ws = workspace
+    if ws is None:
+        ws = _workspace(moe_attention_prompt_workspace_bytes(Tq, Tk, n, nq, nkv, D), q.device)
+    else:
+        _on_gpu("moe_attention_prompt: workspace", ws, gpu)
+    at = ctypes.addressof
+    _enqueue("moe_attention_prompt", gpu, at(qh), at(kh), at(vh), cq, ck, n, Tq, Tk, nq, nkv, D,
+             D ** -0.5 if scale is None else scale, int(bool(causal)), window, at(yh),
+             None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+             0 if ws is None else ws.numel())
+    return y, lse
+
+
+def moe_attention_decode_workspace_bytes(B: int, n_q_heads: int, cache: KvCache, max_len: int) -> int:
+    key = (B, n_q_heads, max_len)
+    need = cache._need.get(key)
+    if need is None:
+        need = cache._need[key] = lib().moe_attention_decode_workspace_bytes(B, n_q_heads, cache.n_kv_heads,
+                                                                             cache.head_dim, max_len)
+    return need
+
+
+def moe_attention_decode(q: torch.Tensor, cache: KvCache, page_table: torch.Tensor, lens: torch.Tensor,
+                         max_len: Optional[int] = None, scale: Optional[float] = None, window: int = 0,
+                         want_lse: bool = False, out=None, workspace=None):
+    """One new token per sequence: q [B][n_q_heads][head_dim] over the lens[b] cached tokens (int32 [B]) on the pages
+    page_table[b] (int32 [B][width], contiguous rows) -> (y like q, lse fp32 [B][n_q_heads] or None).  max_len (None: the
+    table's width in tokens) bounds the lengths.  scale None: head_dim ** -0.5."""
+    gpu = _gpu(q)
+    B, nq, D = q.shape
+    if cache.index != gpu:
+        raise ValueError(f"moe_attention_decode: q is on GPU {gpu}, the cache on {cache.device}")
+    qh = _heads("moe_attention_decode: q", q, (B, nq, cache.head_dim), gpu)
+    y, lse, yh = _attention_out("moe_attention_decode", q, out, want_lse, gpu)
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        raise ValueError(f"moe_attention_decode: page_table must be int32 [B][width], got {page_table.dtype}")
+    width = page_table.shape[1]
+    stride = _rows("moe_attention_decode: page_table", page_table, (B, width), gpu)
+    if max_len is None:
+        max_len = width * cache.page_size
+    ws = workspace
+    if ws is None:
+        need = moe_attention_decode_workspace_bytes(B, nq, cache, max_len)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _on_gpu("moe_attention_decode: workspace", ws, gpu)
+    _enqueue("moe_attention_decode", gpu, ctypes.addressof(qh), B, nq, cache.at, page_table.data_ptr(), stride, width,
+             _ints("moe_attention_decode: lens", lens, (B,), gpu), max_len, D ** -0.5 if scale is None else scale, window,
+             ctypes.addressof(yh), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+             0 if ws is None else ws.numel())
+    return y, lse
+
+
+# ----------------------------------------------------------------------------------------------------
 class MoELayer:
     """One routed-MoE layer with every intermediate buffer allocated once, so that forward() only
     enqueues the four library calls (capturable in a HIP graph)."""
@@ -910,6 +1151,61 @@ class MoEBlock:
         return moe_combine(self.y_slots, self.weights, out=self.y), residual_out
 
 
+class AttentionBlock:
+    """The attention half of a decoder block, in front of MoEBlock: residual addition and norm, one 4-bit product for q,
+    k and v (W_qkv: n_q_heads query heads, then n_kv_heads key and as many value heads), rotary positions and the cache
+    write, attention.  Its row buffers are allocated once for up to T tokens, workspaces by each call, so a pass captures
+    into a HIP graph.  Passes of one block share its buffers, so they run one after another on one stream.
+
+    prompt(x, residual, positions, slots, cu) attends each sequence over its own rows, decode(x, residual, positions,
+    slots, page_table, lens) each row over its cached tokens, its own (written to slots[b]) among them.  Both -> (attn
+    [T'][n_q_heads * head_dim], residual_out), which MoEBlock.forward takes; x (an MoEBlock's y, or embeddings) and
+    residual are [T'][hidden] for T' <= T tokens."""
+
+    def __init__(self, W_qkv: LinearWeights, T: int, norm: RmsNorm, n_q_heads: int, cache: KvCache,
+                 rope: Optional[Rope] = None, window: int = 0):
+        D, nkv = cache.head_dim, cache.n_kv_heads
+        if W_qkv.n_out != (n_q_heads + 2 * nkv) * D or W_qkv.k_in != norm.hidden:
+            raise ValueError(f"AttentionBlock: {W_qkv.n_out} x {W_qkv.k_in} weights do not fit {n_q_heads} + 2 * {nkv} "
+                             f"heads of {D} and a norm of {norm.hidden}")
+        if cache.act is not torch.bfloat16:
+            raise ValueError("AttentionBlock: 4-bit products take bf16 rows, so the cache is bf16 or mxfp8")
+        self.W_qkv, self.T, self.norm, self.cache, self.rope, self.window = W_qkv, T, norm, cache, rope, window
+        self.n_q_heads = n_q_heads
+        empty = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
+        self.x = empty(T, norm.hidden)
+        self.qkv = torch.empty((T, W_qkv.n_out), dtype=torch.float32, device=cache.device)
+        self.q, self.k, self.v, self.y = empty(T, n_q_heads, D), empty(T, nkv, D), empty(T, nkv, D), empty(T, n_q_heads, D)
+
+    def _front(self, x, residual, positions, slots, residual_out, packed: bool):
+        t = x.shape[0]
+        if t > self.T:
+            raise ValueError(f"AttentionBlock: {t} rows, built for {self.T}")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        moe_add_rms_norm(x, self.norm, residual, out=(self.x[:t], residual_out, None, None))
+        qkv = moe_linear(self.x[:t], self.W_qkv, out=self.qkv[:t]).view(t, -1, self.cache.head_dim)
+        n, m = self.n_q_heads, self.cache.n_kv_heads
+        moe_rope_cache(qkv[:, :n], qkv[:, n:n + m], qkv[:, n + m:], self.rope,
+                       None if self.rope is None else positions, self.cache, slots,
+                       out=(self.q[:t], self.k[:t] if packed else None, self.v[:t] if packed else None))
+        return t, residual_out
+
+    def prompt(self, x: torch.Tensor, residual: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+               cu: torch.Tensor, residual_out: Optional[torch.Tensor] = None):
+        t, residual_out = self._front(x, residual, positions, slots, residual_out, True)
+        moe_attention_prompt(self.q[:t], self.k[:t], self.v[:t], cu, window=self.window, out=(self.y[:t], None))
+        return self.y[:t].view(t, -1), residual_out
+
+    def decode(self, x: torch.Tensor, residual: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+               page_table: torch.Tensor, lens: torch.Tensor, max_len: Optional[int] = None,
+               residual_out: Optional[torch.Tensor] = None):
+        t, residual_out = self._front(x, residual, positions, slots, residual_out, False)
+        moe_attention_decode(self.q[:t], self.cache, page_table, lens, max_len, window=self.window,
+                             out=(self.y[:t], None))
+        return self.y[:t].view(t, -1), residual_out
+
+
 class FixedShapeLayer:
     """A routed-MoE layer run at fixed row shapes (Cascadia Sec. 3.2): for each supported shape S
     the five calls (route, pad, bucket, expert FFN, combine) on S rows are captured once in a HIP
@@ -996,4 +1292,6 @@ __all__ = ["moe_route", "moe_route_sigmoid", "moe_route_bucket", "moe_route_buck
            "moe_route_workspace_bytes", "moe_bucket_workspace_bytes", "moe_expert_ffn_workspace_bytes",
            "moe_row_shape", "moe_pad_rows", "ExpertWeights", "Buckets", "MoELayer", "FixedShapeLayer", "MoEError",
            "moe_select_experts", "moe_route_grouped", "moe_add_rms_norm", "moe_linear", "moe_linear_workspace_bytes",
-           "moe_expert_ffn_mx_codes", "RouteRule", "RmsNorm", "LinearWeights", "MoEBlock", "lib"]
+           "moe_expert_ffn_mx_codes", "RouteRule", "RmsNorm", "LinearWeights", "MoEBlock", "lib",
+           "moe_rope_cache", "moe_attention_prompt", "moe_attention_prompt_workspace_bytes", "moe_attention_decode",
+           "moe_attention_decode_workspace_bytes", "Rope", "KvCache", "AttentionBlock"]

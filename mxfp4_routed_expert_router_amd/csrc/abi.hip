@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include "../../include/moe.h"
+#include "attention.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -813,6 +814,267 @@ moe_status moe_linear(const void* x, moe_act_dtype x_dtype, int64_t x_row_stride
   a.y_stride = y_row_stride;
   a.ws = workspace;
   return hip_status(moe::launch_linear(a, (hipStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------------------------
+// Attention: rotary positions and the cache write, prompts, one new token per sequence.
+namespace {
+
+constexpr int64_t kMostStride = (int64_t)1 << 40;  // of heads, tokens and pages, in values
+constexpr int64_t kMostBlocks = (int64_t)1 << 23;  // workgroups of a launch: fewer than 2^32 threads
+
+inline bool al_stride(int64_t s, int64_t values) { return s % values == 0; }
+// Strides and alignment of a moe_heads; unit: values that its rows' bases have to be a multiple of (1: a value).
+moe_status check_heads(const moe_heads& h, int unit) {
+  if (!known_dt(h.dtype)) return MOE_ERR_DTYPE;
+  if (h.token_stride < 0 || h.head_stride < 0 || h.token_stride > kMostStride || h.head_stride > kMostStride)
+    return MOE_ERR_SHAPE;
+  if (!al_value(h.p, h.dtype)) return MOE_ERR_ALIGN;
+  if (unit > 1 && (!al16(h.p) || !al_stride(h.token_stride, unit) || !al_stride(h.head_stride, unit)))
+    return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+moe_status check_cache(const moe_kv_cache& c) {
+  if (c.fmt != MOE_KV_BF16 && c.fmt != MOE_KV_FP16 && c.fmt != MOE_KV_MXFP8) return MOE_ERR_DTYPE;
+  const bool mx = c.fmt == MOE_KV_MXFP8;
+  if (!c.k || !c.v || (mx && (!c.k_scales || !c.v_scales))) return MOE_ERR_NULL;
+  if (!mx && (c.k_scales || c.v_scales)) return MOE_ERR_DTYPE;
+  if (c.n_pages < 1 || c.page_size < 1 || (int64_t)c.n_pages * c.page_size > INT_MAX || c.n_kv_heads < 1 ||
+      c.n_kv_heads > MOE_MAX_HEADS || c.head_dim < 8 || c.head_dim > MOE_MAX_HEAD_DIM || c.head_dim % 8 != 0)
+    return MOE_ERR_SHAPE;
+  if (mx && c.head_dim % 32 != 0) return MOE_ERR_BLOCK;
+  for (const int64_t s : {c.page_stride, c.head_stride, c.token_stride})
+    if (s < 0 || s > kMostStride) return MOE_ERR_SHAPE;
+  if (mx)
+    for (const int64_t s : {c.s_page_stride, c.s_head_stride, c.s_token_stride})
+      if (s < 0 || s > kMostStride) return MOE_ERR_SHAPE;
+  const int unit = mx ? 16 : 8;
+  if (!al16(c.k) || !al16(c.v) || !al_stride(c.page_stride, unit) || !al_stride(c.head_stride, unit) ||
+      !al_stride(c.token_stride, unit))
+    return MOE_ERR_ALIGN;
+  return MOE_OK;
+}
+moe_status check_head_counts(int n_q_heads, int n_kv_heads, int head_dim) {
+  if (n_q_heads < 1 || n_q_heads > MOE_MAX_HEADS || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || head_dim < 8 ||
+      head_dim > MOE_MAX_HEAD_DIM || head_dim % 8 != 0)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+// Exponents are base 2: a scale whose product with log2(e) leaves fp32 is refused.
+inline bool usable_scale(float s) { return s > 0.0f && finite(s * 1.4426950408889634f); }
+inline float base2_scale(float s) { return (float)((double)s * 1.4426950408889634074); }
+inline moe::HeadsDev heads_dev(const moe_heads* h) {
+  moe::HeadsDev d{};
+  if (h) d = {h->p, h->token_stride, h->head_stride, h->dtype};
+  return d;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T, int n_q_heads, int n_kv_heads,
+                          int head_dim, const moe_heads* q, const moe_heads* k, const moe_heads* v,
+                          const moe_heads* q_out, const moe_heads* k_out, const moe_heads* v_out,
+                          const moe_kv_cache* cache, const int32_t* slots, void* stream) {
+  if (T == 0) return MOE_OK;
+  if (T < 0 || n_q_heads < 0 || n_q_heads > MOE_MAX_HEADS || n_kv_heads < 0 || n_kv_heads > MOE_MAX_HEADS ||
+      n_q_heads + n_kv_heads < 1 || head_dim < 8 || head_dim > MOE_MAX_HEAD_DIM || head_dim % 8 != 0)
+    return MOE_ERR_SHAPE;
+  if ((int64_t)T * (n_q_heads + 2 * n_kv_heads) > (int64_t)1 << 27) return MOE_ERR_SHAPE;
+  if ((n_q_heads > 0 && (!q || !q_out)) || (n_kv_heads > 0 && !k) || ((v_out || cache) && !v)) return MOE_ERR_NULL;
+  if (n_kv_heads > 0 && !k_out && !v_out && !cache) return MOE_ERR_NULL;
+  if ((cache != nullptr) != (slots != nullptr)) return MOE_ERR_NULL;
+  if ((rope != nullptr) != (positions != nullptr)) return MOE_ERR_NULL;
+  const moe_heads* in[3] = {n_q_heads > 0 ? q : nullptr, n_kv_heads > 0 ? k : nullptr, n_kv_heads > 0 ? v : nullptr};
+  const moe_heads* out[3] = {n_q_heads > 0 ? q_out : nullptr, n_kv_heads > 0 ? k_out : nullptr,
+                             n_kv_heads > 0 ? v_out : nullptr};
+  int dt = -1;
+  for (int i = 0; i < 3; ++i) {
+    for (const moe_heads* h : {in[i], out[i]}) {
+      if (!h) continue;
+      if (!h->p) return MOE_ERR_NULL;
+      const moe_status st = check_heads(*h, 1);
+      if (st != MOE_OK) return st;
+    }
+    if (!in[i]) continue;
+    if (dt >= 0 && in[i]->dtype != dt) return MOE_ERR_DTYPE;
+    dt = in[i]->dtype;
+    if (out[i] && out[i]->p == in[i]->p && (out[i]->dtype != dt || out[i]->token_stride != in[i]->token_stride ||
+                                            out[i]->head_stride != in[i]->head_stride))
+      return MOE_ERR_SHAPE;
+  }
+  moe::RopeArgs a{};
+  if (rope) {
+    if (!rope->cos || !rope->sin) return MOE_ERR_NULL;
+    if (rope->n_positions < 1 || rope->rotary_dim < 2 || rope->rotary_dim > head_dim || rope->rotary_dim % 2 != 0)
+      return MOE_ERR_SHAPE;
+    if (rope->pairs != MOE_ROPE_HALVES && rope->pairs != MOE_ROPE_NEIGHBOURS) return MOE_ERR_DTYPE;
+    if (!al4(rope->cos) || !al4(rope->sin) || !al4(positions)) return MOE_ERR_ALIGN;
+    a.cos = rope->cos;
+    a.sin = rope->sin;
+    a.positions = positions;
+    a.n_positions = rope->n_positions;
+    a.R = rope->rotary_dim;
+    a.neighbours = rope->pairs == MOE_ROPE_NEIGHBOURS;
+  }
+  a.page_size = moe::fast_div(1);
+  if (cache) {
+    const moe_status st = check_cache(*cache);
+    if (st != MOE_OK) return st;
+    if (cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim) return MOE_ERR_SHAPE;
+    if (!al4(slots)) return MOE_ERR_ALIGN;
+    a.fmt = cache->fmt;
+    a.n_slots = cache->n_pages * cache->page_size;
+    a.slots = slots;
+    a.cache_k = cache->k;
+    a.cache_v = cache->v;
+    a.scale_k = cache->k_scales;
+    a.scale_v = cache->v_scales;
+    a.c_page = cache->page_stride;
+    a.c_head = cache->head_stride;
+    a.c_token = cache->token_stride;
+    a.s_page = cache->s_page_stride;
+    a.s_head = cache->s_head_stride;
+    a.s_token = cache->s_token_stride;
+    a.page_size = moe::fast_div((uint32_t)cache->page_size);
+  }
+  a.T = T;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.D = head_dim;
+  a.x_dt = dt;
+  for (int i = 0; i < 3; ++i) {
+    a.in[i] = heads_dev(in[i]);
+    a.out[i] = heads_dev(out[i]);
+  }
+  a.n_rows = moe::fast_div((uint32_t)(n_q_heads + 2 * n_kv_heads));
+  return hip_status(moe::launch_rope(a, (hipStream_t)stream));
+}
+
+size_t moe_attention_prompt_workspace_bytes(int Tq, int Tk, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim) {
+  if (Tq <= 0 || Tk < 0 || n_seqs <= 0 || check_head_counts(n_q_heads, n_kv_heads, head_dim) != MOE_OK) return 0;
+  return round_up(moe::prompt_workspace_bytes(Tq, Tk, n_seqs, n_q_heads, n_kv_heads, head_dim), 256);
+}
+
+moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const moe_heads* v, const int32_t* cu_q,
+                                const int32_t* cu_k, int n_seqs, int Tq, int Tk, int n_q_heads, int n_kv_heads,
+                                int head_dim, float scale, int causal, int window, const moe_heads* y, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (Tq == 0 || n_seqs == 0) return MOE_OK;
+  if (Tq < 0 || Tk < 0 || n_seqs < 0) return MOE_ERR_SHAPE;
+  moe_status st = check_head_counts(n_q_heads, n_kv_heads, head_dim);
+  if (st != MOE_OK) return st;
+  if (!q || !k || !v || !y || !cu_q || !cu_k || !q->p || !y->p || (Tk > 0 && (!k->p || !v->p))) return MOE_ERR_NULL;
+  for (const moe_heads* h : {q, k, v, y}) {
+    if (h->dtype != q->dtype || (h->dtype != MOE_DT_BF16 && h->dtype != MOE_DT_FP16)) return MOE_ERR_DTYPE;
+    if ((st = check_heads(*h, 8)) != MOE_OK) return st;
+  }
+  if (!usable_scale(scale) || window < 0 || (window > 0 && !causal)) return MOE_ERR_SHAPE;
+  // rows of a key-value head, and keys one behind another's last query, are 31-bit numbers
+  if ((int64_t)Tq * n_q_heads > INT_MAX || (int64_t)Tq + Tk > INT_MAX || n_seqs > 1 << 20) return MOE_ERR_SHAPE;
+  if (!al4(cu_q) || !al4(cu_k) || (lse && !al4(lse))) return MOE_ERR_ALIGN;
+  if (((int64_t)Tq * n_q_heads / 32 + (int64_t)n_seqs * n_kv_heads) > kMostBlocks) return MOE_ERR_SHAPE;
+  const size_t need = moe_attention_prompt_workspace_bytes(Tq, Tk, n_seqs, n_q_heads, n_kv_heads, head_dim);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!al16(workspace)) return MOE_ERR_ALIGN;
+  moe::PromptArgs a{};
+  a.q = (const uint16_t*)q->p;
+  a.k = (const uint16_t*)k->p;
+  a.v = (const uint16_t*)v->p;
+  a.y = (uint16_t*)y->p;
+  a.lse = lse;
+  a.q_ts = q->token_stride;
+  a.q_hs = q->head_stride;
+  a.k_ts = k->token_stride;
+  a.k_hs = k->head_stride;
+  a.v_ts = v->token_stride;
+  a.v_hs = v->head_stride;
+  a.y_ts = y->token_stride;
+  a.y_hs = y->head_stride;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.n_seqs = n_seqs;
+  a.Tq = Tq;
+  a.Tk = Tk;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.D = head_dim;
+  a.f16 = q->dtype == MOE_DT_FP16;
+  a.G = moe::fast_div((uint32_t)(n_q_heads / n_kv_heads));
+  a.c = base2_scale(scale);
+  a.causal = causal != 0;
+  a.window = window;
+  a.ws = workspace;
+  return hip_status(moe::launch_prompt(a, (hipStream_t)stream));
+}
+
+size_t moe_attention_decode_workspace_bytes(int B, int n_q_heads, int n_kv_heads, int head_dim, int max_len) {
+  if (B <= 0 || max_len <= 0 || check_head_counts(n_q_heads, n_kv_heads, head_dim) != MOE_OK) return 0;
+  return round_up(moe::decode_workspace_bytes(B, n_q_heads, n_kv_heads, head_dim, max_len), 256);
+}
+
+moe_status moe_attention_decode(const moe_heads* q, int B, int n_q_heads, const moe_kv_cache* cache,
+                                const int32_t* page_table, int64_t table_stride, int table_width, const int32_t* lens,
+                                int max_len, float scale, int window, const moe_heads* y, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  if (B == 0) return MOE_OK;
+  if (!cache || !q || !y) return MOE_ERR_NULL;
+  if (B < 0) return MOE_ERR_SHAPE;
+  moe_status st = check_cache(*cache);
+  if (st != MOE_OK) return st;
+  if ((st = check_head_counts(n_q_heads, cache->n_kv_heads, cache->head_dim)) != MOE_OK) return st;
+  if (!q->p || !y->p || !lens || (!page_table && max_len > 0)) return MOE_ERR_NULL;
+  const int dt = cache->fmt == MOE_KV_FP16 ? MOE_DT_FP16 : MOE_DT_BF16;
+  if (q->dtype != dt || y->dtype != dt) return MOE_ERR_DTYPE;
+  if ((st = check_heads(*q, 8)) != MOE_OK || (st = check_heads(*y, 8)) != MOE_OK) return st;
+  if (!usable_scale(scale) || window < 0 || max_len < 0 || table_width < 0 ||
+      max_len > (int64_t)table_width * cache->page_size || table_stride < 0 || table_stride > kMostStride)
+    return MOE_ERR_SHAPE;
+  if ((int64_t)B * n_q_heads > kMostBlocks) return MOE_ERR_SHAPE;
+  if (!al4(page_table) || !al4(lens) || (lse && !al4(lse))) return MOE_ERR_ALIGN;
+  const size_t need =
+      moe_attention_decode_workspace_bytes(B, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!al16(workspace)) return MOE_ERR_ALIGN;
+  moe::DecodeArgs a{};
+  a.q = (const uint16_t*)q->p;
+  a.y = (uint16_t*)y->p;
+  a.lse = lse;
+  a.q_ts = q->token_stride;
+  a.q_hs = q->head_stride;
+  a.y_ts = y->token_stride;
+  a.y_hs = y->head_stride;
+  a.B = B;
+  a.Hq = n_q_heads;
+  a.Hkv = cache->n_kv_heads;
+  a.D = cache->head_dim;
+  a.G = n_q_heads / cache->n_kv_heads;
+  a.f16 = dt == MOE_DT_FP16;
+  a.table = page_table;
+  a.table_stride = table_stride;
+  a.lens = lens;
+  a.max_len = max_len;
+  a.width = table_width;
+  a.window = window;
+  a.n_pages = cache->n_pages;
+  a.fmt = cache->fmt;
+  a.cache_k = cache->k;
+  a.cache_v = cache->v;
+  a.scale_k = cache->k_scales;
+  a.scale_v = cache->v_scales;
+  a.c_page = cache->page_stride;
+  a.c_head = cache->head_stride;
+  a.c_token = cache->token_stride;
+  a.s_page = cache->s_page_stride;
+  a.s_head = cache->s_head_stride;
+  a.s_token = cache->s_token_stride;
+  a.page_size = moe::fast_div((uint32_t)cache->page_size);
+  a.c = base2_scale(scale);
+  a.ws = workspace;
+  return hip_status(moe::launch_decode(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,96 @@
+// What the prompt and the decode attention share: 16-bit MFMA operands, base-2 exponentials, and the partial results of
+// key ranges that several workgroups share.
+//
+// A row (one query head of one token) over keys j: s_j = c q.k_j with c = scale * log2(e), m >= max s_j - 8,
+// l = sum 2^(s_j - m), O = sum 2^(s_j - m) v_j; then y = O / l and lse = (m + log2 l) ln 2.  Parts of a row's keys join
+// by M = max m, l = sum l_p 2^(m_p - M), O likewise.
+#pragma once
+#include "launch.hpp"
+#include "values.hpp"
+
+namespace moe {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <bool F16>
+__device__ __forceinline__ f32x16 mfma_32x32x16(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (F16) return __builtin_amdgcn_mfma_f32_32x32x16_f16(bitcast<f16x8>(a), bitcast<f16x8>(b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(bitcast<bf16x8>(a), bitcast<bf16x8>(b), c, 0, 0, 0);
+}
+template <bool F16>
+__device__ __forceinline__ f32x4 mfma_16x16x32(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (F16) return __builtin_amdgcn_mfma_f32_16x16x32_f16(bitcast<f16x8>(a), bitcast<f16x8>(b), c, 0, 0, 0);
+  else return __builtin_amdgcn_mfma_f32_16x16x32_bf16(bitcast<bf16x8>(a), bitcast<bf16x8>(b), c, 0, 0, 0);
+}
+// Two fp32 values as a dword of 16-bit ones, rounded to nearest even.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if constexpr (F16) return bitcast<uint32_t>(f16x2{(_Float16)a, (_Float16)b});
+  else return bitcast<uint32_t>(bf16x2{(__bf16)a, (__bf16)b});
+}
+__device__ __forceinline__ float unpack16(uint32_t w, int half, bool f16) {
+  const uint16_t b = (uint16_t)(half ? w >> 16 : w);
+  return f16 ? Val<MOE_DT_FP16>::get(b) : Val<MOE_DT_BF16>::get(b);
+}
+
+// Four keys of a 16-bit [key][d] tile in LDS for one d per lane: sixteen lanes give the addresses of four keys' rows of
+// sixteen values (lane i: row i / 4, values 4 (i % 4) ..), lane i gets value i of the four rows.
+__device__ __forceinline__ u32x2 lds_read_tr(const void* p) {
+  return bitcast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+}
+
+// Partial results in a workspace: (m, l) of every row and part, then O.
+struct AttnParts {
+  float* ml;  // [rows][parts][2]
+  float* o;   // [rows][parts][D]
+  int parts;
+};
+inline size_t attn_parts_bytes(int64_t rows, int parts, int D) {
+  return parts > 1 ? (size_t)rows * parts * (size_t)(D + 2) * 4 : 0;
+}
+inline AttnParts attn_parts(void* ws, int64_t rows, int parts) {
+  AttnParts p;
+  p.ml = (float*)ws;
+  p.o = parts > 1 ? (float*)ws + 2 * rows * parts : nullptr;
+  p.parts = parts;
+  return p;
+}
+
+__device__ __forceinline__ AttnParts attn_parts_dev(void* ws, int64_t rows, int parts) {
+  AttnParts p;
+  p.ml = (float*)ws;
+  p.o = (float*)ws + 2 * rows * parts;
+  p.parts = parts;
+  return p;
+}
+struct AttnJoin {
+  AttnParts parts;
+  int64_t rows;        // token * Hq + head
+  int Hq, D, f16;
+  uint16_t* y;
+  int64_t y_ts, y_hs;
+  float* lse;
+  const int32_t* cu_q;  // prompts: rows outside cu_q[0] .. cu_q[n_seqs] are left alone; NULL: all rows
+  int n_seqs;
+};
+hipError_t launch_attn_join(const AttnJoin& j, hipStream_t stream);
+
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^s < d <= 2^(s+1) and mul = ceil(2^(32+s) / d), mul d exceeds
+// 2^(32+s) by less than d <= 2^(s+1), so the quotient is exact for n < 2^31.
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f{d, 0, 0};
+  if (d > 1) {
+    while (((uint64_t)2 << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)((((uint64_t)1 << (32 + f.shift)) + d - 1) / d);
+  }
+  return f;
+}
+__device__ __forceinline__ uint32_t div_by(FastDiv f, uint32_t n) {
+  return f.d == 1 ? n : __umulhi(n, f.mul) >> f.shift;
+}
+
+}  // namespace moe

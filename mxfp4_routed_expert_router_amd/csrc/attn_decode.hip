@@ -1,0 +1,388 @@
+// Attention of one new token per sequence over a paged cache, split over the cache's length and joined.
+//
+// A workgroup takes a sequence's key-value head, up to sixteen of its query heads and a range of its keys; its waves
+// take 32 keys at a time, each with a running maximum and sum of its own, and join at the end through LDS.  S^T = K Q^T
+// puts a head into a column (lane & 15), so maxima, sums and rescaling stay in a lane but for two exchanges, and P^T is
+// the right operand of O^T = V^T P^T as it stands, rounded to a high and a low 16-bit part: the cache's bytes bound the
+// kernel, so the second product costs nothing and only the output is rounded.  K goes from the cache into MFMA layout; V
+// has the same layout on arrival and turns in a part of LDS that is the wave's own.  The next keys are on their way
+// while a tile is computed.
+//
+// 16-bit caches are operands as they are, E4M3 codes times a power of two are exact in bf16.
+#include <algorithm>
+
+#include "attention.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kDecodeWaves = 4, kWaveKeys = 32;
+
+template <int FMT, int DP>
+struct DecodeLoads {  // one tile of K or V as it is stored: lane (r = lane & 15, g = lane >> 4) has rows r and 16 + r
+  static constexpr int N = FMT == MOE_KV_MXFP8 ? DP / 64 : DP / 32;  // 16-byte loads of a row
+  u32x4 q[2][N];
+  uint32_t sc[2][FMT == MOE_KV_MXFP8 ? N : 1];  // MXFP8: scale code of each load's block
+};
+
+// First value of the operand of step st for lanes of group g.
+template <int FMT>
+__device__ __forceinline__ int operand_d(int st, int g) {
+  return FMT == MOE_KV_MXFP8 ? 64 * (st >> 1) + 16 * g + 8 * (st & 1) : 32 * st + 8 * g;
+}
+
+template <int FMT, int DP, bool EXACT>
+__device__ __forceinline__ void load_rows(DecodeLoads<FMT, DP>& t, const void* base, const uint8_t* scales,
+                                          const int64_t (&at)[2], const int64_t (&sat)[2], int g, int D) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int n = 0; n < DecodeLoads<FMT, DP>::N; ++n) {
+      const int d = FMT == MOE_KV_MXFP8 ? 64 * n + 16 * g : 32 * n + 8 * g;
+      t.q[h][n] = u32x4{0, 0, 0, 0};
+      if (EXACT || d < D)
+        t.q[h][n] = __builtin_nontemporal_load(
+            reinterpret_cast<const u32x4*>((const char*)base + at[h] + (FMT == MOE_KV_MXFP8 ? d : 2 * d)));
+      if constexpr (FMT == MOE_KV_MXFP8) {
+        t.sc[h][n] = 0;
+        if (EXACT || d < D) t.sc[h][n] = scales[sat[h] + (d >> 5)];
+      }
+    }
+}
+// The operand of step st, row half h.
+template <int FMT, int DP>
+__device__ __forceinline__ u32x4 operand(const DecodeLoads<FMT, DP>& t, int h, int st) {
+  if constexpr (FMT == MOE_KV_MXFP8) {
+    const float s = e8m0_to_f32(t.sc[h][st >> 1]);
+    u32x4 r;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t c = t.q[h][st >> 1][2 * (st & 1) + w];
+      r[2 * w] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
+      r[2 * w + 1] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
+    }
+    return r;
+  } else {
+    return t.q[h][st];
+  }
+}
+
+// Place (16-byte chunk) of chunk c of key `row` in a wave's V tile: sixteen rows' chunks of one column fall into
+// different banks on the way in, the 32-byte pieces of four consecutive rows on the way out.
+template <int DP>
+__device__ __forceinline__ int v_chunk(int row, int c) {
+  if constexpr (DP % 128 == 0) return c ^ (((row & 3) << 1) | ((row >> 2) & 1) | (((row >> 3) & 1) << 3));
+  else return c ^ (((row >> 1) & 1) << 1 | ((row >> 2) & 1) | (((row >> 3) & 1) << 2));
+}
+
+template <int FMT, int DP, bool EXACT>
+__global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs a) {
+  constexpr bool F16 = FMT == MOE_KV_FP16;
+  constexpr int ST = DP / 32, CT = DP / 16, W = kDecodeWaves;
+  __shared__ __attribute__((aligned(16))) u32x4 vt[W][kWaveKeys * DP / 8];  // V tiles; in the end O of the waves
+  __shared__ float stat[W][2][16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int m_tiles = (a.G + 15) >> 4, per_part = a.Hkv * m_tiles;
+  const int unit = blockIdx.x / per_part, in = blockIdx.x - unit * per_part;
+  const int b = unit / a.parts, part = unit - b * a.parts;
+  const int kvh = in / m_tiles, head0 = (in - kvh * m_tiles) * 16, heads = min(16, a.G - head0);
+  const int len = min(max(a.lens[b], 0), a.max_len);
+  const int lo = a.window > 0 ? max(0, len - a.window) : 0;
+  const int64_t from64 = lo + (int64_t)part * a.part_keys;
+  const int from = (int)min(from64, (int64_t)len), to = (int)min(from64 + a.part_keys, (int64_t)len);
+  const int64_t row = (int64_t)b * a.Hq + kvh * a.G + head0 + r;  // this column's output row
+  const bool mine = r < heads;
+  const AttnParts parts = attn_parts_dev(a.ws, (int64_t)a.B * a.Hq, a.parts);
+  const int64_t slot = row * a.parts + part;
+  if (a.parts > 1 && from >= to) {  // nothing here
+    if (wave == 0 && g == 0 && mine) {
+      parts.ml[2 * slot] = -INFINITY;
+      parts.ml[2 * slot + 1] = 0.0f;
+    }
+    return;
+  }
+  const int32_t* table = a.table + (int64_t)b * a.table_stride;
+
+  u32x4 qf[ST];
+  const uint16_t* qp = a.q + (int64_t)b * a.q_ts + (int64_t)(kvh * a.G + head0 + min(r, heads - 1)) * a.q_hs;
+#pragma unroll
+  for (int st = 0; st < ST; ++st) {
+    const int d = operand_d<FMT>(st, g);
+    qf[st] = u32x4{0, 0, 0, 0};
+    if (EXACT || d < a.D) qf[st] = ld16(qp + d);
+  }
+
+  // Rows of a tile: key numbers, pages from the table, byte offsets.  A key past the range or on a page that is none
+  // reads the first page and counts as masked.
+  int page[2], off[2];
+  bool in_range[2];
+  const auto look_up = [&](int j0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = j0 + 16 * h + r;
+      in_range[h] = j < to;
+      const int jj = min(j, to - 1);
+      const int p = (int)div_by(a.page_size, (uint32_t)jj);
+      off[h] = jj - p * (int)a.page_size.d;
+      page[h] = table[p];
+    }
+  };
+  int64_t at[2], sat[2];
+  bool ok[2];
+  const auto place = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const bool there = (uint32_t)page[h] < (uint32_t)a.n_pages;
+      ok[h] = in_range[h] && there;
+      const int64_t p = there ? page[h] : 0;
+      at[h] = p * a.c_page + (int64_t)off[h] * a.c_token + (int64_t)kvh * a.c_head;
+      sat[h] = p * a.s_page + (int64_t)off[h] * a.s_token + (int64_t)kvh * a.s_head;
+      if (FMT != MOE_KV_MXFP8) at[h] *= 2;
+    }
+  };
+
+  f32x4 o[CT];
+#pragma unroll
+  for (int i = 0; i < CT; ++i) o[i] = f32x4{0, 0, 0, 0};
+  float m = -INFINITY, l = 0.0f;
+  const float c = a.c;
+  constexpr int kStep = W * kWaveKeys;
+  const int start = from + wave * kWaveKeys;
+  DecodeLoads<FMT, DP> k, v;
+  u32x4* mine_v = vt[wave];
+  if (start < to) {
+    look_up(start);
+    place();
+    load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
+    load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
+    look_up(min(start + kStep, to - 1));
+  }
+  for (int j0 = start; j0 < to; j0 += kStep) {
+    const bool now[2] = {ok[0], ok[1]};
+    const bool more = j0 + kStep < to;
+    f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) s[h] = mfma_16x16x32<F16>(operand<FMT, DP>(k, h, st), qf[st], s[h]);
+    if (more) {
+      place();
+      load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t seen = (uint32_t)__ballot(now[h]) >> (4 * g);  // (lanes 0-15 hold the sixteen rows' bits)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[h][e] = (seen >> e) & 1 ? s[h][e] : -INFINITY;
+        top = fmaxf(top, s[h][e]);
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, kWave));
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    const float next = fmaxf(m, top);
+    const float f = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - next) * c);
+    const float base = next == -INFINITY ? 0.0f : next * c;
+    m = next;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) o[i] *= f;
+    u32x4 ph, pl;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e], c, -base));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e + 1], c, -base));
+        l += e0 + e1;
+        const uint32_t hi = pack16<F16>(e0, e1);
+        ph[2 * h + (e >> 1)] = hi;
+        pl[2 * h + (e >> 1)] = pack16<F16>(e0 - unpack16(hi, 0, F16), e1 - unpack16(hi, 1, F16));
+      }
+    // V through LDS (rows of masked keys as zeros: 0 * NaN is no zero)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int st = 0; st < ST; ++st) {
+        u32x4 w = operand<FMT, DP>(v, h, st);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) w[x] = now[h] ? w[x] : 0u;
+        const int vr = 16 * h + r;
+        mine_v[vr * (DP / 8) + v_chunk<DP>(r, operand_d<FMT>(st, g) >> 3)] = w;
+      }
+    if (more) {
+      load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
+      look_up(min(j0 + 2 * kStep, to - 1));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const char* vb = reinterpret_cast<const char*>(mine_v);
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      u32x4 w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int key = 4 * g + (r >> 2), d = 16 * i + 4 * (r & 3);
+        const u32x2 t = lds_read_tr(vb + (16 * h + key) * (2 * DP) + (v_chunk<DP>(key, d >> 3) << 4) + ((d & 7) << 1));
+        w[2 * h] = t[0];
+        w[2 * h + 1] = t[1];
+      }
+      o[i] = mfma_16x16x32<F16>(w, pl, o[i]);
+      o[i] = mfma_16x16x32<F16>(w, ph, o[i]);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // The waves' parts: reference and sum of each head, then O scaled to the common reference and added
+  l += __shfl_xor(l, 16, kWave);
+  l += __shfl_xor(l, 32, kWave);
+  if (g == 0) {
+    stat[wave][0][r] = m;
+    stat[wave][1][r] = l;
+  }
+  __syncthreads();
+  float all = -INFINITY, sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < W; ++w) all = fmaxf(all, stat[w][0][r]);
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    sum += stat[w][0][r] == -INFINITY ? stat[w][1][r] : stat[w][1][r] * __builtin_amdgcn_exp2f((stat[w][0][r] - all) * c);
+  const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - all) * c);
+  // O of a wave as [16 heads][DP] fp32, in its V tile's place: float 4-groups of a head's row take turns with the head
+  float* ow = reinterpret_cast<float*>(mine_v);
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+    *reinterpret_cast<f32x4*>(ow + r * DP + ((4 * i + g) ^ (r & 7)) * 4) = o[i] * f;
+  __syncthreads();
+  // thread: head tid / 16, values in groups of four
+  const int oh = tid >> 4;
+  const float* o0 = reinterpret_cast<const float*>(&vt[0][0]);
+  const float total = __shfl(sum, oh & 15, kWave), top = __shfl(all, oh & 15, kWave);
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int64_t orow = (int64_t)b * a.Hq + kvh * a.G + head0 + oh;
+  if (oh < heads) {
+#pragma unroll
+    for (int u = 0; u < DP / 64; ++u) {
+      const int q4 = 16 * u + (tid & 15), d = 4 * q4;
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        x += *reinterpret_cast<const f32x4*>(o0 + w * (16 * DP) + oh * DP + ((q4 ^ (oh & 7)) << 2));
+      if (!EXACT && d >= a.D) continue;
+      if (a.parts > 1) {
+        *reinterpret_cast<f32x4*>(parts.o + (orow * a.parts + part) * a.D + d) = x;
+      } else {
+        u32x2 y = {pack16<F16>(x[0] * inv, x[1] * inv), pack16<F16>(x[2] * inv, x[3] * inv)};
+        *reinterpret_cast<u32x2*>(a.y + (int64_t)b * a.y_ts + (int64_t)(kvh * a.G + head0 + oh) * a.y_hs + d) = y;
+      }
+    }
+    if ((tid & 15) == 0) {
+      if (a.parts > 1) {
+        parts.ml[2 * (orow * a.parts + part)] = top * c;
+        parts.ml[2 * (orow * a.parts + part) + 1] = total;
+      } else if (a.lse) {
+        a.lse[orow] = total == 0.0f ? -INFINITY : (top * c + __builtin_amdgcn_logf(total)) * kLn2;
+      }
+    }
+  }
+}
+
+// One wave per row joins its parts in order.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnJoin a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.rows) return;
+  const int64_t t = row / a.Hq;
+  const int h = (int)(row - t * a.Hq);
+  if (a.cu_q && (t < a.cu_q[0] || t >= a.cu_q[a.n_seqs])) return;
+  const float* ml = a.parts.ml + 2 * row * a.parts.parts;
+  const int P = a.parts.parts;
+  float top = -INFINITY;
+  for (int p = 0; p < P; ++p) top = fmaxf(top, ml[2 * p]);
+  const int d = 4 * lane;
+  float total = 0.0f;
+  f32x4 x = {0, 0, 0, 0};
+  for (int p = 0; p < P; ++p) {
+    const float l = ml[2 * p + 1];
+    if (l == 0.0f) continue;
+    const float f = __builtin_amdgcn_exp2f(ml[2 * p] - top);
+    total += l * f;
+    if (d < a.D) x += *reinterpret_cast<const f32x4*>(a.parts.o + (row * P + p) * a.D + d) * f;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  if (d < a.D) {
+    const u32x2 y = {(uint32_t)f32_to_16(x[0] * inv, a.f16) | (uint32_t)f32_to_16(x[1] * inv, a.f16) << 16,
+                     (uint32_t)f32_to_16(x[2] * inv, a.f16) | (uint32_t)f32_to_16(x[3] * inv, a.f16) << 16};
+    *reinterpret_cast<u32x2*>(a.y + t * a.y_ts + (int64_t)h * a.y_hs + d) = y;
+  }
+  if (lane == 0 && a.lse) a.lse[row] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+struct DecodePlan {
+  int parts, part_keys;
+};
+DecodePlan plan_decode(int B, int Hq, int Hkv, int D, int max_len) {
+  constexpr int kBlockKeys = kDecodeWaves * kWaveKeys;
+  const int64_t units = (int64_t)B * Hkv * ((Hq / Hkv + 15) / 16);
+  int64_t parts = (1024 + units - 1) / units;
+  const int64_t most = (max_len + kBlockKeys - 1) / kBlockKeys;
+  parts = std::max<int64_t>(1, std::min(parts, most));
+  DecodePlan p;
+  const int64_t keys = (max_len + parts - 1) / parts;
+  p.part_keys = (int)((keys + kBlockKeys - 1) / kBlockKeys * kBlockKeys);
+  p.part_keys = std::max(p.part_keys, kBlockKeys);
+  p.parts = (int)std::max<int64_t>(1, (max_len + (int64_t)p.part_keys - 1) / p.part_keys);
+  return p;
+}
+
+template <int FMT>
+void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
+#define MOE_DECODE(DP)                                                                    \
+  (a.D == DP ? decode_kernel<FMT, DP, true><<<g, 64 * kDecodeWaves, 0, stream>>>(a)       \
+             : decode_kernel<FMT, DP, false><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
+  if (a.D <= 64) MOE_DECODE(64);
+  else if (a.D <= 128) MOE_DECODE(128);
+  else if (a.D <= 192) MOE_DECODE(192);
+  else MOE_DECODE(256);
+#undef MOE_DECODE
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len) {
+  return attn_parts_bytes((int64_t)B * Hq, plan_decode(B, Hq, Hkv, D, max_len).parts, D);
+}
+
+hipError_t launch_attn_join(const AttnJoin& j, hipStream_t stream) {
+  attn_join_kernel<<<dim3((unsigned)((j.rows + 3) / 4)), 256, 0, stream>>>(j);
+  return hipGetLastError();
+}
+
+hipError_t launch_decode(DecodeArgs a, hipStream_t stream) {
+  const DecodePlan p = plan_decode(a.B, a.Hq, a.Hkv, a.D, a.max_len);
+  a.parts = p.parts;
+  a.part_keys = p.part_keys;
+  const dim3 g((unsigned)((int64_t)a.B * p.parts * a.Hkv * ((a.G + 15) / 16)));
+  if (a.fmt == MOE_KV_BF16) launch_decode_fmt<MOE_KV_BF16>(a, g, stream);
+  else if (a.fmt == MOE_KV_FP16) launch_decode_fmt<MOE_KV_FP16>(a, g, stream);
+  else launch_decode_fmt<MOE_KV_MXFP8>(a, g, stream);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess || p.parts == 1) return err;
+  AttnJoin j{};
+  j.parts = attn_parts(a.ws, (int64_t)a.B * a.Hq, p.parts);
+  j.rows = (int64_t)a.B * a.Hq;
+  j.Hq = a.Hq;
+  j.D = a.D;
+  j.f16 = a.fmt == MOE_KV_FP16;
+  j.y = a.y;
+  j.y_ts = a.y_ts;
+  j.y_hs = a.y_hs;
+  j.lse = a.lse;
+  return launch_attn_join(j, stream);
+}
+
+}  // namespace moe

@@ -166,6 +166,69 @@ struct LinArgs {
 size_t linear_workspace_bytes(int fmt, int T, int N, int K);
 hipError_t launch_linear(const LinArgs& a, hipStream_t stream);
 
+// ---- attention: rotary positions and cache write, prompts, decoding ----
+struct FastDiv {  // n / d for n < 2^31 (attention.hpp)
+  uint32_t d, mul, shift;
+};
+struct HeadsDev {  // moe_heads; p NULL: absent
+  void* p;
+  int64_t ts, hs;
+  int dt;
+};
+struct RopeArgs {
+  const float *cos, *sin;     // [n_positions][R / 2]
+  const int32_t* positions;   // [T], or NULL (R = 0)
+  int n_positions, R, neighbours;
+  int T, Hq, Hkv, D, x_dt;
+  HeadsDev in[3], out[3];     // q, k, v
+  int fmt, n_slots;           // cache: moe_kv_format, pages * page size
+  const int32_t* slots;       // [T], or NULL: no cache
+  void *cache_k, *cache_v;
+  uint8_t *scale_k, *scale_v;
+  int64_t c_page, c_head, c_token, s_page, s_head, s_token;
+  FastDiv page_size;
+  FastDiv n_rows;             // Hq + 2 Hkv
+  int runs, rows_per_wave;    // set by the launch
+};
+hipError_t launch_rope(RopeArgs a, hipStream_t stream);
+
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* y;
+  float* lse;                 // [Tq][Hq] or NULL
+  int64_t q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, y_ts, y_hs;
+  const int32_t *cu_q, *cu_k;
+  int n_seqs, Tq, Tk, Hq, Hkv, D, f16;
+  FastDiv G;                  // Hq / Hkv
+  float c;                    // scale * log2(e)
+  int causal, window;
+  void* ws;
+  int parts, part_keys;       // set by the launch: workgroups that share a row's keys, and keys of each
+};
+size_t prompt_workspace_bytes(int Tq, int Tk, int n_seqs, int Hq, int Hkv, int D);
+hipError_t launch_prompt(PromptArgs a, hipStream_t stream);
+
+struct DecodeArgs {
+  const uint16_t* q;
+  uint16_t* y;
+  float* lse;                 // [B][Hq] or NULL
+  int64_t q_ts, q_hs, y_ts, y_hs;
+  int B, Hq, Hkv, D, G, f16;
+  const int32_t* table;       // [B] rows of `width` page numbers
+  int64_t table_stride;
+  const int32_t* lens;
+  int max_len, width, window, n_pages, fmt;
+  const void *cache_k, *cache_v;
+  const uint8_t *scale_k, *scale_v;
+  int64_t c_page, c_head, c_token, s_page, s_head, s_token;
+  FastDiv page_size;
+  float c;
+  void* ws;
+  int parts, part_keys;       // set by the launch
+};
+size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len);
+hipError_t launch_decode(DecodeArgs a, hipStream_t stream);
+
 // ---- combine ----
 hipError_t launch_combine(const float* y_slots, const float* weights, int T, int k_total, int H, float* y,
                           hipStream_t stream);
