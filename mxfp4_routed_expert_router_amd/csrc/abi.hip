@@ -975,6 +975,8 @@ moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const mo
   if (!usable_scale(scale) || window < 0 || (window > 0 && !causal)) return MOE_ERR_SHAPE;
   // rows of a key-value head, and keys one behind another's last query, are 31-bit numbers
   if ((int64_t)Tq * n_q_heads > INT_MAX || (int64_t)Tq + Tk > INT_MAX || n_seqs > 1 << 20) return MOE_ERR_SHAPE;
+  // (64 keys of a tile are addressed with 32-bit offsets)
+  if (k->token_stride >= 1 << 24 || v->token_stride >= 1 << 24) return MOE_ERR_SHAPE;
   if (!al4(cu_q) || !al4(cu_k) || (lse && !al4(lse))) return MOE_ERR_ALIGN;
   if (((int64_t)Tq * n_q_heads / 32 + (int64_t)n_seqs * n_kv_heads) > kMostBlocks) return MOE_ERR_SHAPE;
   const size_t need = moe_attention_prompt_workspace_bytes(Tq, Tk, n_seqs, n_q_heads, n_kv_heads, head_dim);

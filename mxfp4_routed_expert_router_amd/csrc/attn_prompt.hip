@@ -74,11 +74,18 @@ __device__ __forceinline__ Piece find_piece(const PromptArgs& a, int slot, int r
   return Piece{0, 0, 0, 0, -1};
 }
 
-// Whether a dword of two 16-bit values holds an infinity or NaN.
+// The 16-bit values of a dword that are infinite or NaN, as a mask.
 template <bool F16>
-__device__ __forceinline__ bool not_finite(uint32_t w) {
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
-  return (w & e) == e || (w & (e << 16)) == (e << 16);
+  return ((w & e) == e ? 0xFFFFu : 0u) | ((w & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
+}
+
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+__device__ __forceinline__ u32x4 lds_16(uint32_t at) { return *(lds_u32x4*)(uintptr_t)at; }
+__device__ __forceinline__ u32x2 lds_tr(uint32_t at) {
+  return bitcast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at));
 }
 
 template <bool F16, int DP, bool EXACT, int NW, int PER_SIMD>
@@ -135,38 +142,75 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     for (int i = tid; i < 4 * BN * CH; i += 64 * NW) (&lds[0][0][0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
+  // Tiles go from memory straight into LDS, a wave 1 KB a time.  Where a round of the workgroup is a multiple of sixteen
+  // rows, a lane's place in a row is the same in all rounds and a round's rows are a scalar further.
+  constexpr int ROUNDS = BN * CH / (64 * NW), STEP = 64 * NW / CH;
+  constexpr bool REGULAR = (64 * NW) % CH == 0 && STEP % 16 == 0;
+  const auto place = [&](int u, int64_t ts, bool v, int last) {  // byte offset of round u's 16 bytes from the tile's first row
+    const int p = u * 64 * NW + tid, row = p / CH, cc = p % CH;
+    const int c = cc ^ (v ? swizzle_v<DP>(row) : swizzle_k<DP>(row));
+    return (EXACT || 8 * c < a.D) ? (uint32_t)min(row, last) * (uint32_t)(2 * ts) + 16 * c : ~0u;
+  };
+  const uint32_t k_off = place(0, a.k_ts, false, BN), v_off = place(0, a.v_ts, true, BN);
+  const auto put = [&](const uint16_t* base, uint32_t off, u32x4* to) {
+    if (EXACT || off != ~0u)
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const char*)base + off),
+                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+  };
   const auto load_tile = [&](int buf, int j0) {
+    const uint16_t *kt = kp + j0 * a.k_ts, *vt = vp + j0 * a.v_ts;
+    u32x4 *dk = &lds[buf][0][64 * wave], *dv = &lds[buf][1][64 * wave];
+    if (REGULAR && j0 + BN <= pc.nk) {
 #pragma unroll
-    for (int u = 0; u < BN * CH / (64 * NW); ++u) {
-      const int p = u * 64 * NW + tid, row = p / CH, cc = p % CH;
-      const int key = min(j0 + row, pc.nk - 1);  // rows past the last key repeat it, and are masked
-      const int ck = cc ^ swizzle_k<DP>(row), cv = cc ^ swizzle_v<DP>(row);
-      u32x4* dk = &lds[buf][0][u * 64 * NW + 64 * wave];
-      u32x4* dv = &lds[buf][1][u * 64 * NW + 64 * wave];
-      if (EXACT || 8 * ck < a.D)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kp + (int64_t)key * a.k_ts + 8 * ck),
-                                         (__attribute__((address_space(3))) void*)dk, 16, 0, 0);
-      if (EXACT || 8 * cv < a.D)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(vp + (int64_t)key * a.v_ts + 8 * cv),
-                                         (__attribute__((address_space(3))) void*)dv, 16, 0, 0);
+      for (int u = 0; u < ROUNDS; ++u) {
+        put(kt + u * STEP * a.k_ts, k_off, dk + u * 64 * NW);
+        put(vt + u * STEP * a.v_ts, v_off, dv + u * 64 * NW);
+      }
+    } else {  // rows past the last key repeat it, and are masked
+#pragma unroll
+      for (int u = 0; u < ROUNDS; ++u) {
+        put(kt, place(u, a.k_ts, false, pc.nk - 1 - j0), dk + u * 64 * NW);
+        put(vt, place(u, a.v_ts, true, pc.nk - 1 - j0), dv + u * 64 * NW);
+      }
     }
   };
+
+  // LDS addresses.  Rows are multiples of kSpan bytes and a swizzle stays inside one, so a step inside a span is an
+  // exclusive-or of a lane's address, and one to another span an addition.
+  constexpr int kSpan = DP % 128 == 0 ? 256 : 128, KS = kSpan / 32, VS = kSpan / 64;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&lds[0][0][0];
+  constexpr uint32_t kTile = BN * CH * 16;
+  const uint32_t k_at = lds0 + col * (2 * DP) + ((half ^ swizzle_k<DP>(col)) << 4);
+  const int vi = lane & 15, v_row = 4 * half + (vi >> 2);
+  const uint32_t v_at = lds0 + kTile + v_row * (2 * DP) +
+                        (((2 * ((lane >> 4) & 1) + ((vi & 3) >> 1)) ^ swizzle_v<DP>(v_row)) << 4) + ((vi & 1) << 3);
 
   f32x16 o[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-  float m = -INFINITY, l = 0.0f;  // m: reference of the exponents (at most 8 below the maximum), l: this lane's keys
-  const float c = a.c, slack = 8.0f / c;
+  // m: reference of the exponents (base 2, scaled; at most 8 below the maximum), l: sum over this lane's keys
+  float m = -INFINITY, l = 0.0f;
+  const float c = a.c;
 
-  if (n_tiles > 0) load_tile(0, b_lo);
-  for (int it = 0; it < n_tiles; ++it) {
-    const int j0 = b_lo + it * BN, buf = it & 1;
-    __syncthreads();  // tile `it` is there, and nobody reads the other buffer any more
-    if (it + 1 < n_tiles) load_tile(buf ^ 1, j0 + BN);
-    if (j0 >= w_hi || j0 + BN <= w_lo) continue;  // nothing of the tile is the wave's
-
+  const auto v_frag = [&](uint32_t buf, int ks, int dt) {
+    const uint32_t at = ((v_at + buf) ^ (uint32_t)((dt % VS) << 6)) + dt / VS * kSpan + ks * (16 * 2 * DP);
+    const u32x2 x = lds_tr(at), y = lds_tr(at + 8 * 2 * DP);
+    return u32x4{x[0], x[1], y[0], y[1]};
+  };
+  const auto tile = [&](bool masked, uint32_t buf, int j0) {
+    // 0 * infinity is no zero: a masked key's value must not reach a row, so values that are not finite go by themselves
+    bool wild = false;
+    if (__builtin_expect(masked, 0)) {
+      uint32_t bad = 0;
+#pragma unroll
+      for (int u = 0; u < BN * CH / 64; ++u) {
+        const u32x4 w = lds_16(lds0 + buf + kTile + (64 * u + lane) * 16);
+        bad |= not_finite<F16>(w[0]) | not_finite<F16>(w[1]) | not_finite<F16>(w[2]) | not_finite<F16>(w[3]);
+      }
+      wild = __any(bad != 0);
+    }
     f32x16 s[KT];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
@@ -175,102 +219,103 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 #pragma unroll
     for (int st = 0; st < ST; ++st)
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const u32x4 kf = lds[buf][0][(32 * kt + col) * CH + ((2 * st + half) ^ swizzle_k<DP>(col))];
-        s[kt] = mfma_32x32x16<F16>(kf, qf[st], s[kt]);
+      for (int kt = 0; kt < KT; ++kt)
+        s[kt] = mfma_32x32x16<F16>(
+            lds_16(((k_at + buf) ^ (uint32_t)((st % KS) << 5)) + st / KS * kSpan + kt * (32 * 2 * DP)), qf[st], s[kt]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float top = -INFINITY;
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[kt][r] = __builtin_fmaf(s[kt][r], c, -base);
       }
-    const bool masked = j0 + BN > w_hi_min || j0 < w_lo_max;
-    if (masked) {
+    if (__builtin_expect(masked, 0)) {
+      int lo_j = lo - j0 - 4 * half, hi_j = hi - j0 - 4 * half;
+      asm volatile("" : "+v"(lo_j), "+v"(hi_j));  // (nothing of this block ahead of its branch)
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int j = j0 + 32 * kt + 8 * (r >> 2) + 4 * half + (r & 3);
-          s[kt][r] = j >= lo && j < hi ? s[kt][r] : -INFINITY;
+          const int j = 32 * kt + 8 * (r >> 2) + (r & 3);
+          s[kt][r] = j >= lo_j && j < hi_j ? s[kt][r] : -INFINITY;
         }
     }
-    float top = s[0][0];
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kt][r]);
     top = other_half_max(top);
     // The reference rises only when some row's maximum passes it by more than 2^8: every exponential stays below that
-    if (__any(top > m + slack || (m == -INFINITY && top > m))) {
-      const float next = fmaxf(m, top);
-      const float f = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - next) * c);
-      m = next;
+    if (__builtin_expect(__any(top > 8.0f || (m == -INFINITY && top > -INFINITY)), 0)) {
+      float up = m == -INFINITY ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
+      asm volatile("" : "+v"(up));  // (nothing of this rare block ahead of its branch)
+      const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up);  // (before the first key O and l are zero)
+      m = m == -INFINITY ? top : m + up;
       l *= f;
 #pragma unroll
       for (int i = 0; i < DT; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[i][r] *= f;
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[kt][r] -= up;
     }
-    const float base = m == -INFINITY ? 0.0f : m * c;
     u32x4 pf[2 * KT];
     float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
       for (int r = 0; r < 16; r += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r], c, -base));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kt][r + 1], c, -base));
-        part[(r >> 1) & 3] += e0 + e1;
+        const float e0 = __builtin_amdgcn_exp2f(s[kt][r]);
+        const float e1 = __builtin_amdgcn_exp2f(s[kt][r + 1]);
+        part[r & 2] += e0;
+        part[(r & 2) + 1] += e1;
         pf[2 * kt + (r >> 3)][(r >> 1) & 3] = pack16<F16>(e0, e1);
       }
     l += (part[0] + part[1]) + (part[2] + part[3]);
-
-    const char* vt = reinterpret_cast<const char*>(&lds[buf][1][0]);
-    const int vi = lane & 15, vsub = 16 * ((lane >> 4) & 1);
-    const auto v_frag = [&](int ks, int dt) {
-      u32x4 w;
+    if (__builtin_expect(!wild, 1)) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * ks + 8 * e + 4 * half + (vi >> 2), d = 32 * dt + vsub + 4 * (vi & 3);
-        const u32x2 t = lds_read_tr(vt + row * (2 * DP) + (((d >> 3) ^ swizzle_v<DP>(row)) << 4) + ((d & 7) << 1));
-        w[2 * e] = t[0];
-        w[2 * e + 1] = t[1];
-      }
-      return w;
-    };
-    bool wild = false;
-    if (masked) {  // 0 * infinity is no zero: a masked key's value must not reach a row
+      for (int ks = 0; ks < 2 * KT; ++ks)
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[dt] = mfma_32x32x16<F16>(v_frag(buf, ks, dt), pf[ks], o[dt]);
+    } else {
 #pragma unroll
       for (int ks = 0; ks < 2 * KT; ++ks)
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
-          const u32x4 w = v_frag(ks, dt);
-          wild |= not_finite<F16>(w[0]) || not_finite<F16>(w[1]) || not_finite<F16>(w[2]) || not_finite<F16>(w[3]);
+          u32x4 w = v_frag(buf, ks, dt);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] &= ~not_finite<F16>(w[x]);
+          o[dt] = mfma_32x32x16<F16>(w, pf[ks], o[dt]);
         }
-      wild = __any(wild);
-    }
-    if (!wild) {
+#pragma unroll 1
+      for (int kk = 0; kk < BN; ++kk) {  // what was left out, into the rows that see it
+        const bool seen = j0 + kk >= lo && j0 + kk < hi;
 #pragma unroll
-      for (int ks = 0; ks < 2 * KT; ++ks)
+        for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[dt] = mfma_32x32x16<F16>(v_frag(ks, dt), pf[ks], o[dt]);
-    } else {  // one key at a time, into the rows that see it
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const u32x2 w = *(lds_u32x2*)(uintptr_t)(lds0 + buf + kTile + kk * (2 * DP) +
+                                          (((4 * dt + q4) ^ swizzle_v<DP>(kk)) << 4) + 8 * half);
 #pragma unroll
-      for (int ks = 0; ks < 2 * KT; ++ks)
-        for (int kk = 0; kk < 16; ++kk) {
-          const int j = j0 + 16 * ks + kk;
-          const bool seen = j >= lo && j < hi;
-          u32x4 pm, vm;
-          const int e = kk - 4 * half;  // element of this half's operand: 0-3, or 8-11 for its second four
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int at = 8 * (w >> 1) + 2 * (w & 1);
-            pm[w] = (e == at ? 0xFFFFu : 0u) | (e == at + 1 ? 0xFFFF0000u : 0u);
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t bad = not_finite<F16>(w[x >> 1]) & (x & 1 ? 0xFFFF0000u : 0xFFFFu);
+              o[dt][4 * q4 + x] += seen && bad ? unpack16(w[x >> 1], x & 1, F16) : 0.0f;
+            }
           }
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) {
-            vm = v_frag(ks, dt) & pm;
-            const f32x16 n = mfma_32x32x16<F16>(vm, pf[ks] & pm, o[dt]);
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[dt][r] = seen ? n[r] : o[dt][r];
-          }
-        }
+      }
     }
+  };
+
+  if (n_tiles > 0) load_tile(0, b_lo);
+  for (int it = 0; it < n_tiles; ++it) {
+    const int j0 = b_lo + it * BN, buf = it & 1;
+    __syncthreads();  // tile `it` is there, and nobody reads the other buffer any more
+    if (it + 1 < n_tiles) load_tile(buf ^ 1, j0 + BN);
+    if (j0 >= w_hi || j0 + BN <= w_lo) continue;  // nothing of the tile is the wave's
+    tile(j0 + BN > w_hi_min || j0 < w_lo_max, buf * 2 * kTile, j0);
   }
 
   l = other_half_sum(l);
@@ -281,7 +326,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     const AttnParts w = attn_parts_dev(a.ws, (int64_t)a.Tq * a.Hq, a.parts);
     const int64_t at = orow * a.parts + blockIdx.y;
     if (half == 0) {
-      w.ml[2 * at] = m * c;
+      w.ml[2 * at] = m;
       w.ml[2 * at + 1] = l;
     }
     if (n_tiles == 0) return;
@@ -314,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
       const int d = 32 * dt + 8 * (q4 + half);
       if (mine && (EXACT || d < a.D)) st16(yp + d, w);
     }
-  if (mine && half == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m * c + __builtin_amdgcn_logf(l)) * kLn2;
+  if (mine && half == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <bool F16, int DP, int NW, int PER_SIMD>
