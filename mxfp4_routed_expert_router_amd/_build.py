@@ -21,6 +21,14 @@ HIPCC_FLAGS = [
 ]
 
 
+# Flags of single sources.  The attention loops have rare branches that a whole wave takes together; left to itself the
+# compiler rewrites them as if lanes could part there, and keeps two copies of the accumulators for it (a prompt's loop:
+# 256 registers and 64 moves a tile, 184 and none with the flag).
+SOURCE_FLAGS = {
+    "attn_prompt.hip": ["-mllvm", "-structurizecfg-skip-uniform-regions"],
+}
+
+
 def hipcc() -> str:
     for c in (os.environ.get("HIPCC"), "/opt/rocm/bin/hipcc", shutil.which("hipcc")):
         if c and os.path.exists(c):
@@ -29,7 +37,7 @@ def hipcc() -> str:
 
 
 def _compile(src: str, obj: str) -> None:
-    cmd = [hipcc(), *HIPCC_FLAGS, "-c", src, "-o", obj]
+    cmd = [hipcc(), *HIPCC_FLAGS, *SOURCE_FLAGS.get(os.path.basename(src), []), "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -40,6 +40,9 @@ __device__ __forceinline__ float other_half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// (a ballot is uniform to the compiler, __any() is not: its branches would keep both sides' values in registers)
+__device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
+
 struct Piece {  // a workgroup's rows
   int q0, nq, k0, nk, tile;  // tile < 0: none
 };
@@ -209,7 +212,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
         const u32x4 w = lds_16(lds0 + buf + kTile + (64 * u + lane) * 16);
         bad |= not_finite<F16>(w[0]) | not_finite<F16>(w[1]) | not_finite<F16>(w[2]) | not_finite<F16>(w[3]);
       }
-      wild = __any(bad != 0);
+      wild = wave_any(bad != 0);
     }
     f32x16 s[KT];
 #pragma unroll
@@ -238,7 +241,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int j = 32 * kt + 8 * (r >> 2) + (r & 3);
-          s[kt][r] = j >= lo_j && j < hi_j ? s[kt][r] : -INFINITY;
+          s[kt][r] = ((j >= lo_j) & (j < hi_j)) ? s[kt][r] : -INFINITY;
         }
     }
 #pragma unroll
@@ -247,16 +250,14 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kt][r]);
     top = other_half_max(top);
     // The reference rises only when some row's maximum passes it by more than 2^8: every exponential stays below that
-    if (__builtin_expect(__any(top > 8.0f || (m == -INFINITY && top > -INFINITY)), 0)) {
+    if (__builtin_expect(wave_any((top > 8.0f) | ((m == -INFINITY) & (top > -INFINITY))), 0)) {
       float up = m == -INFINITY ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
       asm volatile("" : "+v"(up));  // (nothing of this rare block ahead of its branch)
       const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up);  // (before the first key O and l are zero)
       m = m == -INFINITY ? top : m + up;
       l *= f;
 #pragma unroll
-      for (int i = 0; i < DT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[i][r] *= f;
+      for (int i = 0; i < DT; ++i) o[i] *= f;
 #pragma unroll
       for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -292,9 +293,10 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
         }
 #pragma unroll 1
       for (int kk = 0; kk < BN; ++kk) {  // what was left out, into the rows that see it
-        const bool seen = j0 + kk >= lo && j0 + kk < hi;
+        const bool seen = (j0 + kk >= lo) & (j0 + kk < hi);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
+        for (int dt = 0; dt < DT; ++dt) {
+          f32x16 more;
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) {
             const u32x2 w = *(lds_u32x2*)(uintptr_t)(lds0 + buf + kTile + kk * (2 * DP) +
@@ -302,9 +304,11 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const uint32_t bad = not_finite<F16>(w[x >> 1]) & (x & 1 ? 0xFFFF0000u : 0xFFFFu);
-              o[dt][4 * q4 + x] += seen && bad ? unpack16(w[x >> 1], x & 1, F16) : 0.0f;
+              more[4 * q4 + x] = (seen & (bad != 0)) ? unpack16(w[x >> 1], x & 1, F16) : 0.0f;
             }
           }
+          o[dt] += more;
+        }
       }
     }
   };
