@@ -21,14 +21,17 @@ namespace {
 constexpr int kTileKeys = 64, kPartKeys = 512;
 
 // Swizzles (in 16-byte chunks) of a tile's rows of DP values.  K: sixteen consecutive rows' chunks of one column fall
-// into different banks.  V: so do the 32-byte pieces of four consecutive rows that a transposing read takes.
+// into different banks.  V: so do the 32-byte pieces of four consecutive rows that a transposing read takes.  Each stays
+// inside aligned spans of 256, 128 or 64 bytes, of which a row is a multiple.
+template <int DP>
+constexpr int kSpanOf = DP % 128 == 0 ? 256 : (DP % 64 == 0 ? 128 : 64);
 template <int DP>
 __device__ __forceinline__ int swizzle_k(int row) {
-  return DP % 128 == 0 ? row & 15 : (row >> 1) & 7;
+  return kSpanOf<DP> == 256 ? row & 15 : (kSpanOf<DP> == 128 ? (row >> 1) & 7 : (row >> 2) & 3);
 }
 template <int DP>
 __device__ __forceinline__ int swizzle_v(int row) {
-  return DP % 128 == 0 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+  return kSpanOf<DP> == 256 ? (row & 3) << 2 : (kSpanOf<DP> == 128 ? ((row >> 1) & 1) << 2 : 0);
 }
 
 __device__ __forceinline__ float other_half_max(float v) {
@@ -42,6 +45,20 @@ __device__ __forceinline__ float other_half_sum(float v) {
 
 // (a ballot is uniform to the compiler, __any() is not: its branches would keep both sides' values in registers)
 __device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
+
+// Next in a block's order: READS LDS reads; a matrix product with TRANS exponentials, VALU vector instructions and READS
+// LDS reads behind it.
+template <int READS>
+__device__ __forceinline__ void then_read() {
+  __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+}
+template <int TRANS, int VALU, int READS>
+__device__ __forceinline__ void then_multiply() {
+  __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+  if constexpr (TRANS > 0) __builtin_amdgcn_sched_group_barrier(0x400, TRANS, 0);
+  if constexpr (VALU > 0) __builtin_amdgcn_sched_group_barrier(0x2, VALU, 0);
+  if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+}
 
 struct Piece {  // a workgroup's rows
   int q0, nq, k0, nk, tile;  // tile < 0: none
@@ -95,6 +112,9 @@ template <bool F16, int DP, bool EXACT, int NW, int PER_SIMD>
 __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a) {
   constexpr int CH = DP / 8;          // 16-byte chunks of a row
   constexpr int BN = kTileKeys, KT = BN / 32, DT = DP / 32, ST = DP / 16;
+  // Whether the next tile's scores run between a tile's exponentials.  Heads of 128 gain by it (16384 tokens: 4340 -> 4130
+  // us); heads of 64 have less to multiply, and the registers of the second set of scores cost them a third wave (33 -> 44).
+  constexpr bool kAhead = DP > 64;
   constexpr int ROWS = 32 * NW;
   __shared__ __attribute__((aligned(1024))) u32x4 lds[2][2][BN * CH];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -145,42 +165,44 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     for (int i = tid; i < 4 * BN * CH; i += 64 * NW) (&lds[0][0][0])[i] = u32x4{0, 0, 0, 0};
     __syncthreads();
   }
-  // Tiles go from memory straight into LDS, a wave 1 KB a time.  Where a round of the workgroup is a multiple of sixteen
-  // rows, a lane's place in a row is the same in all rounds and a round's rows are a scalar further.
+  // Tiles go from memory straight into LDS, a wave 1 KB a time.  A lane's place in a row repeats after KEEP rounds (where
+  // those are sixteen rows), which are a scalar further; else each round has an offset of its own.
   constexpr int ROUNDS = BN * CH / (64 * NW), STEP = 64 * NW / CH;
-  constexpr bool REGULAR = (64 * NW) % CH == 0 && STEP % 16 == 0;
+  constexpr bool WHOLE = (64 * NW) % CH == 0 && (STEP % 16 == 0 || 16 % STEP == 0);
+  constexpr int KEEP = !WHOLE ? ROUNDS : (STEP >= 16 ? 1 : 16 / STEP);
   const auto place = [&](int u, int64_t ts, bool v, int last) {  // byte offset of round u's 16 bytes from the tile's first row
     const int p = u * 64 * NW + tid, row = p / CH, cc = p % CH;
     const int c = cc ^ (v ? swizzle_v<DP>(row) : swizzle_k<DP>(row));
     return (EXACT || 8 * c < a.D) ? (uint32_t)min(row, last) * (uint32_t)(2 * ts) + 16 * c : ~0u;
   };
-  const uint32_t k_off = place(0, a.k_ts, false, BN), v_off = place(0, a.v_ts, true, BN);
+  uint32_t k_off[KEEP], v_off[KEEP];
+#pragma unroll
+  for (int u = 0; u < KEEP; ++u) {
+    k_off[u] = place(u, a.k_ts, false, BN);
+    v_off[u] = place(u, a.v_ts, true, BN);
+  }
   const auto put = [&](const uint16_t* base, uint32_t off, u32x4* to) {
     if (EXACT || off != ~0u)
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const char*)base + off),
                                        (__attribute__((address_space(3))) void*)to, 16, 0, 0);
   };
-  const auto load_tile = [&](int buf, int j0) {
-    const uint16_t *kt = kp + j0 * a.k_ts, *vt = vp + j0 * a.v_ts;
-    u32x4 *dk = &lds[buf][0][64 * wave], *dv = &lds[buf][1][64 * wave];
-    if (REGULAR && j0 + BN <= pc.nk) {
+  const auto load_tile = [&](int buf, int v, const uint16_t* rows, int64_t ts, const uint32_t* off, int j0) {
+    const uint16_t* from = rows + j0 * ts;
+    u32x4* to = &lds[buf][v][64 * wave];
+    if (DP <= 192 && j0 + BN <= pc.nk) {  // (kept offsets would not fit the registers of heads beyond 192: 345 -> 381 us)
 #pragma unroll
-      for (int u = 0; u < ROUNDS; ++u) {
-        put(kt + u * STEP * a.k_ts, k_off, dk + u * 64 * NW);
-        put(vt + u * STEP * a.v_ts, v_off, dv + u * 64 * NW);
-      }
+      for (int u = 0; u < ROUNDS; ++u)
+        put(from + u / KEEP * KEEP * STEP * ts, off[u % KEEP], to + u * 64 * NW);
     } else {  // rows past the last key repeat it, and are masked
 #pragma unroll
-      for (int u = 0; u < ROUNDS; ++u) {
-        put(kt, place(u, a.k_ts, false, pc.nk - 1 - j0), dk + u * 64 * NW);
-        put(vt, place(u, a.v_ts, true, pc.nk - 1 - j0), dv + u * 64 * NW);
-      }
+      for (int u = 0; u < ROUNDS; ++u) put(from, place(u, ts, v != 0, pc.nk - 1 - j0), to + u * 64 * NW);
     }
   };
+  const auto load_k = [&](int t) { load_tile(t & 1, 0, kp, a.k_ts, k_off, b_lo + t * BN); };
+  const auto load_v = [&](int t) { load_tile(t & 1, 1, vp, a.v_ts, v_off, b_lo + t * BN); };
 
-  // LDS addresses.  Rows are multiples of kSpan bytes and a swizzle stays inside one, so a step inside a span is an
-  // exclusive-or of a lane's address, and one to another span an addition.
-  constexpr int kSpan = DP % 128 == 0 ? 256 : 128, KS = kSpan / 32, VS = kSpan / 64;
+  // LDS addresses.  A step inside a span is an exclusive-or of a lane's address, one to another span an addition.
+  constexpr int kSpan = kSpanOf<DP>, KS = kSpan / 32, VS = kSpan / 64;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&lds[0][0][0];
   constexpr uint32_t kTile = BN * CH * 16;
   const uint32_t k_at = lds0 + col * (2 * DP) + ((half ^ swizzle_k<DP>(col)) << 4);
@@ -202,7 +224,32 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     const u32x2 x = lds_tr(at), y = lds_tr(at + 8 * 2 * DP);
     return u32x4{x[0], x[1], y[0], y[1]};
   };
-  const auto tile = [&](bool masked, uint32_t buf, int j0) {
+  const auto scores = [&](f32x16 (&s)[KT], uint32_t buf) {
+#pragma unroll
+    for (int st = 0; st < ST; ++st)
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        const u32x4 kf = lds_16(((k_at + buf) ^ (uint32_t)((st % KS) << 5)) + st / KS * kSpan + kt * (32 * 2 * DP));
+        f32x16 zero;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+        s[kt] = mfma_32x32x16<F16>(kf, qf[st], st == 0 ? zero : s[kt]);
+      }
+  };
+  // Tile t from its scores on (kAhead: with the scores of the tile after it, `after`, on the way).
+  const auto tile = [&](f32x16 (&s)[KT], f32x16 (&after)[KT], int t) {
+    const int j0 = b_lo + t * BN;
+    const uint32_t buf = (t & 1) * 2 * kTile, buf_after = buf ^ (2 * kTile);
+    // V of tile t is there, K too (kAhead: of tile t + 1), and nobody reads what the next loads replace any more
+    __syncthreads();
+    if (t + 1 + kAhead < n_tiles) load_k(t + 1 + kAhead);
+    if (t + 1 < n_tiles) load_v(t + 1);
+    if (j0 >= w_hi || j0 + BN <= w_lo) {  // nothing of the tile is the wave's
+      if constexpr (kAhead) scores(after, buf_after);
+      return;
+    }
+    if constexpr (!kAhead) scores(s, buf);
+    const bool masked = j0 + BN > w_hi_min || j0 < w_lo_max;
     // 0 * infinity is no zero: a masked key's value must not reach a row, so values that are not finite go by themselves
     bool wild = false;
     if (__builtin_expect(masked, 0)) {
@@ -214,25 +261,11 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
       }
       wild = wave_any(bad != 0);
     }
-    f32x16 s[KT];
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[kt][r] = 0.0f;
-#pragma unroll
-    for (int st = 0; st < ST; ++st)
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
-        s[kt] = mfma_32x32x16<F16>(
-            lds_16(((k_at + buf) ^ (uint32_t)((st % KS) << 5)) + st / KS * kSpan + kt * (32 * 2 * DP)), qf[st], s[kt]);
     const float base = m == -INFINITY ? 0.0f : m;
-    float top = -INFINITY;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[kt][r] = __builtin_fmaf(s[kt][r], c, -base);
-      }
+      for (int r = 0; r < 16; ++r) s[kt][r] = __builtin_fmaf(s[kt][r], c, -base);
     if (__builtin_expect(masked, 0)) {
       int lo_j = lo - j0 - 4 * half, hi_j = hi - j0 - 4 * half;
       asm volatile("" : "+v"(lo_j), "+v"(hi_j));  // (nothing of this block ahead of its branch)
@@ -244,6 +277,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
           s[kt][r] = ((j >= lo_j) & (j < hi_j)) ? s[kt][r] : -INFINITY;
         }
     }
+    float top = -INFINITY;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -263,27 +297,58 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 #pragma unroll
         for (int r = 0; r < 16; ++r) s[kt][r] -= up;
     }
-    u32x4 pf[2 * KT];
-    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 pf[2 * KT], vf[DT];
+    const auto exponentials = [&](int ks) {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-      for (int r = 0; r < 16; r += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(s[kt][r]);
-        const float e1 = __builtin_amdgcn_exp2f(s[kt][r + 1]);
-        part[r & 2] += e0;
-        part[(r & 2) + 1] += e1;
-        pf[2 * kt + (r >> 3)][(r >> 1) & 3] = pack16<F16>(e0, e1);
+      for (int e = 0; e < 8; e += 2) {
+        const int r = 8 * (ks & 1) + e;
+        const float e0 = __builtin_amdgcn_exp2f(s[ks >> 1][r]), e1 = __builtin_amdgcn_exp2f(s[ks >> 1][r + 1]);
+        s[ks >> 1][r] = e0;
+        s[ks >> 1][r + 1] = e1;
+        pf[ks][e >> 1] = pack16<F16>(e0, e1);
       }
-    l += (part[0] + part[1]) + (part[2] + part[3]);
+    };
+    if constexpr (kAhead) {
+      scores(after, buf_after);
+#pragma unroll
+      for (int ks = 0; ks < 2 * KT; ++ks) exponentials(ks);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) vf[dt] = v_frag(buf, 0, dt);
+    }
+    if constexpr (kAhead) {  // products between the exponentials, operands four products before their use, then the first V
+      constexpr int N = ST * KT;
+      then_read<4>();
+#pragma unroll
+      for (int i = 0; i < N - 4; ++i) then_multiply<16 * KT / N, 8 * KT / N, 1>();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) then_multiply<16 * KT / N, 8 * KT / N, (DT + 1) / 2>();
+    }
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const auto add = [&](int ks) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[e & 3] += s[ks >> 1][8 * (ks & 1) + e];
+    };
     if (__builtin_expect(!wild, 1)) {
 #pragma unroll
-      for (int ks = 0; ks < 2 * KT; ++ks)
+      for (int ks = 0; ks < 2 * KT; ++ks) {
+        if constexpr (!kAhead) exponentials(ks);
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[dt] = mfma_32x32x16<F16>(v_frag(buf, ks, dt), pf[ks], o[dt]);
+        for (int dt = 0; dt < DT; ++dt) {
+          if constexpr (!kAhead) vf[dt] = v_frag(buf, ks, dt);
+          o[dt] = mfma_32x32x16<F16>(vf[dt], pf[ks], o[dt]);
+          if (kAhead && ks + 1 < 2 * KT) vf[dt] = v_frag(buf, ks + 1, dt);
+        }
+        add(ks);
+      }
+      l += (part[0] + part[1]) + (part[2] + part[3]);
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int i = 0; i < 2 * KT * DT; ++i) then_multiply<0, 2, 2>();
+      }
     } else {
 #pragma unroll
-      for (int ks = 0; ks < 2 * KT; ++ks)
+      for (int ks = 0; ks < 2 * KT; ++ks) {
+        if constexpr (!kAhead) exponentials(ks);
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
           u32x4 w = v_frag(buf, ks, dt);
@@ -291,6 +356,9 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
           for (int x = 0; x < 4; ++x) w[x] &= ~not_finite<F16>(w[x]);
           o[dt] = mfma_32x32x16<F16>(w, pf[ks], o[dt]);
         }
+        add(ks);
+      }
+      l += (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll 1
       for (int kk = 0; kk < BN; ++kk) {  // what was left out, into the rows that see it
         const bool seen = (j0 + kk >= lo) & (j0 + kk < hi);
@@ -313,13 +381,22 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     }
   };
 
-  if (n_tiles > 0) load_tile(0, b_lo);
-  for (int it = 0; it < n_tiles; ++it) {
-    const int j0 = b_lo + it * BN, buf = it & 1;
-    __syncthreads();  // tile `it` is there, and nobody reads the other buffer any more
-    if (it + 1 < n_tiles) load_tile(buf ^ 1, j0 + BN);
-    if (j0 >= w_hi || j0 + BN <= w_lo) continue;  // nothing of the tile is the wave's
-    tile(j0 + BN > w_hi_min || j0 < w_lo_max, buf * 2 * kTile, j0);
+  if (n_tiles > 0) {
+    load_k(0);
+    load_v(0);
+    f32x16 s0[KT], s1[KT];
+    if constexpr (kAhead) {
+      if (n_tiles > 1) load_k(1);
+      __syncthreads();
+      scores(s0, 0);
+      // (behind the last tile the other buffer's scores are computed once more and not used)
+      for (int t = 0; t < n_tiles; t += 2) {
+        tile(s0, s1, t);
+        if (t + 1 < n_tiles) tile(s1, s0, t + 1);
+      }
+    } else {
+      for (int t = 0; t < n_tiles; ++t) tile(s0, s0, t);
+    }
   }
 
   l = other_half_sum(l);
@@ -403,7 +480,8 @@ hipError_t launch_prompt(PromptArgs a, hipStream_t stream) {
   const dim3 g((unsigned)(p.slots * a.Hkv), (unsigned)p.parts);
 #define MOE_PROMPT(DP, NW, OCC) \
   (a.f16 ? launch_exact<true, DP, NW, OCC>(a, g, stream) : launch_exact<false, DP, NW, OCC>(a, g, stream))
-  if (a.D <= 64) MOE_PROMPT(64, 4, 2);
+  if (a.D <= 64) MOE_PROMPT(64, 4, 4);
+  else if (a.D <= 96) MOE_PROMPT(96, 4, 2);
   else if (a.D <= 128) MOE_PROMPT(128, 4, 2);
   else if (a.D <= 192) MOE_PROMPT(192, 4, 1);
   else MOE_PROMPT(256, 4, 1);
