@@ -76,8 +76,8 @@ __device__ __forceinline__ int v_chunk(int row, int c) {
   else return c ^ (((row >> 1) & 1) << 1 | ((row >> 2) & 1) | (((row >> 3) & 1) << 2));
 }
 
-template <int FMT, int DP, bool EXACT>
-__global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs a) {
+template <int FMT, int DP, bool EXACT, int PER_SIMD>
+__global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(DecodeArgs a) {
   constexpr bool F16 = FMT == MOE_KV_FP16;
   constexpr int ST = DP / 32, CT = DP / 16, W = kDecodeWaves;
   __shared__ __attribute__((aligned(16))) u32x4 vt[W][kWaveKeys * DP / 8];  // V tiles; in the end O of the waves
@@ -114,19 +114,15 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
     if (EXACT || d < a.D) qf[st] = ld16(qp + d);
   }
 
-  // Rows of a tile: key numbers, pages from the table, byte offsets.  A key past the range or on a page that is none
-  // reads the first page and counts as masked.
-  int page[2], off[2];
-  bool in_range[2];
+  // Rows of a tile: pages from the table, then byte offsets.  A key past the range or on a page that is none reads the
+  // cache's first row and counts as masked.  Loads return in order, so a tile's pages are asked for before the K and V of
+  // the tile in front of it: their use then waits for neither.
+  int page[2], key[2];
   const auto look_up = [&](int j0) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int j = j0 + 16 * h + r;
-      in_range[h] = j < to;
-      const int jj = min(j, to - 1);
-      const int p = (int)div_by(a.page_size, (uint32_t)jj);
-      off[h] = jj - p * (int)a.page_size.d;
-      page[h] = table[p];
+      key[h] = j0 + 16 * h + r;
+      page[h] = table[div_by(a.page_size, (uint32_t)min(key[h], a.max_len - 1))];
     }
   };
   int64_t at[2], sat[2];
@@ -134,11 +130,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
   const auto place = [&]() {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool there = (uint32_t)page[h] < (uint32_t)a.n_pages;
-      ok[h] = in_range[h] && there;
-      const int64_t p = there ? page[h] : 0;
-      at[h] = p * a.c_page + (int64_t)off[h] * a.c_token + (int64_t)kvh * a.c_head;
-      sat[h] = p * a.s_page + (int64_t)off[h] * a.s_token + (int64_t)kvh * a.s_head;
+      ok[h] = key[h] < to && (uint32_t)page[h] < (uint32_t)a.n_pages;
+      const int64_t p = ok[h] ? page[h] : 0;
+      const int off = ok[h] ? key[h] - (int)(div_by(a.page_size, (uint32_t)key[h]) * a.page_size.d) : 0;
+      at[h] = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
+      sat[h] = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
       if (FMT != MOE_KV_MXFP8) at[h] *= 2;
     }
   };
@@ -155,9 +151,9 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
   if (start < to) {
     look_up(start);
     place();
+    look_up(start + kStep);
     load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
     load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
-    look_up(min(start + kStep, to - 1));
   }
   for (int j0 = start; j0 < to; j0 += kStep) {
     const bool now[2] = {ok[0], ok[1]};
@@ -169,6 +165,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
       for (int h = 0; h < 2; ++h) s[h] = mfma_16x16x32<F16>(operand<FMT, DP>(k, h, st), qf[st], s[h]);
     if (more) {
       place();
+      look_up(j0 + 2 * kStep);
       load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
     }
     float top = -INFINITY;
@@ -213,10 +210,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
         const int vr = 16 * h + r;
         mine_v[vr * (DP / 8) + v_chunk<DP>(r, operand_d<FMT>(st, g) >> 3)] = w;
       }
-    if (more) {
-      load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
-      look_up(min(j0 + 2 * kStep, to - 1));
-    }
+    if (more) load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const char* vb = reinterpret_cast<const char*>(mine_v);
@@ -291,35 +285,47 @@ __global__ __launch_bounds__(64 * kDecodeWaves, 2) void decode_kernel(DecodeArgs
   }
 }
 
-// One wave per row joins its parts in order.
+// A workgroup per row joins its parts: the waves read all references and sums at once, then L lanes take a part's O and
+// 256 / L groups of them the parts in turn, joined in order through LDS.
+template <int L>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnJoin a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= a.rows) return;
+  constexpr int GROUPS = 256 / L;
+  __shared__ f32x4 sum[GROUPS][L];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t row = blockIdx.x;
   const int64_t t = row / a.Hq;
   const int h = (int)(row - t * a.Hq);
   if (a.cu_q && (t < a.cu_q[0] || t >= a.cu_q[a.n_seqs])) return;
-  const float* ml = a.parts.ml + 2 * row * a.parts.parts;
   const int P = a.parts.parts;
-  float top = -INFINITY;
-  for (int p = 0; p < P; ++p) top = fmaxf(top, ml[2 * p]);
-  const int d = 4 * lane;
-  float total = 0.0f;
+  const f32x2* ml = reinterpret_cast<const f32x2*>(a.parts.ml) + row * P;
+  const f32x2 first = lane < P ? ml[lane] : f32x2{-INFINITY, 0.0f};
+  float top = first[0];
+  for (int p = lane + 64; p < P; p += 64) top = fmaxf(top, ml[p][0]);
+  top = wave_max_dpp(top);
+  // (a part without keys has the sum 0, whatever its reference)
+  float total = first[1] == 0.0f ? 0.0f : first[1] * __builtin_amdgcn_exp2f(first[0] - top);
+  for (int p = lane + 64; p < P; p += 64) total += ml[p][1] == 0.0f ? 0.0f : ml[p][1] * __builtin_amdgcn_exp2f(ml[p][0] - top);
+  total = wave_sum_dpp(total);
+  const int g = tid / L, d = 4 * (tid % L);
   f32x4 x = {0, 0, 0, 0};
-  for (int p = 0; p < P; ++p) {
-    const float l = ml[2 * p + 1];
-    if (l == 0.0f) continue;
-    const float f = __builtin_amdgcn_exp2f(ml[2 * p] - top);
-    total += l * f;
-    if (d < a.D) x += *reinterpret_cast<const f32x4*>(a.parts.o + (row * P + p) * a.D + d) * f;
-  }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   if (d < a.D) {
+#pragma unroll 4
+    for (int p = g; p < P; p += GROUPS) {
+      const f32x2 w = ml[p];
+      if (w[1] != 0.0f) x += *reinterpret_cast<const f32x4*>(a.parts.o + (row * P + p) * a.D + d) * __builtin_amdgcn_exp2f(w[0] - top);
+    }
+  }
+  sum[g][tid % L] = x;
+  __syncthreads();
+  if (g == 0 && d < a.D) {
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) x += sum[i][tid];
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     const u32x2 y = {(uint32_t)f32_to_16(x[0] * inv, a.f16) | (uint32_t)f32_to_16(x[1] * inv, a.f16) << 16,
                      (uint32_t)f32_to_16(x[2] * inv, a.f16) | (uint32_t)f32_to_16(x[3] * inv, a.f16) << 16};
     *reinterpret_cast<u32x2*>(a.y + t * a.y_ts + (int64_t)h * a.y_hs + d) = y;
   }
-  if (lane == 0 && a.lse) a.lse[row] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
+  if (tid == 0 && a.lse) a.lse[row] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 struct DecodePlan {
@@ -341,13 +347,13 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int D, int max_len) {
 
 template <int FMT>
 void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
-#define MOE_DECODE(DP)                                                                    \
-  (a.D == DP ? decode_kernel<FMT, DP, true><<<g, 64 * kDecodeWaves, 0, stream>>>(a)       \
-             : decode_kernel<FMT, DP, false><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
-  if (a.D <= 64) MOE_DECODE(64);
-  else if (a.D <= 128) MOE_DECODE(128);
-  else if (a.D <= 192) MOE_DECODE(192);
-  else MOE_DECODE(256);
+#define MOE_DECODE(DP, OCC)                                                                \
+  (a.D == DP ? decode_kernel<FMT, DP, true, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a)   \
+             : decode_kernel<FMT, DP, false, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
+  if (a.D <= 64) MOE_DECODE(64, 4);
+  else if (a.D <= 128) MOE_DECODE(128, 2);
+  else if (a.D <= 192) MOE_DECODE(192, 2);
+  else MOE_DECODE(256, 1);
 #undef MOE_DECODE
 }
 
@@ -358,7 +364,10 @@ size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len) {
 }
 
 hipError_t launch_attn_join(const AttnJoin& j, hipStream_t stream) {
-  attn_join_kernel<<<dim3((unsigned)((j.rows + 3) / 4)), 256, 0, stream>>>(j);
+  const dim3 g((unsigned)j.rows);
+  if (j.D <= 64) attn_join_kernel<16><<<g, 256, 0, stream>>>(j);
+  else if (j.D <= 128) attn_join_kernel<32><<<g, 256, 0, stream>>>(j);
+  else attn_join_kernel<64><<<g, 256, 0, stream>>>(j);
   return hipGetLastError();
 }
 
