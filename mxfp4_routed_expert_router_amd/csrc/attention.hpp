@@ -37,10 +37,31 @@ __device__ __forceinline__ float unpack16(uint32_t w, int half, bool f16) {
   return f16 ? Val<MOE_DT_FP16>::get(b) : Val<MOE_DT_BF16>::get(b);
 }
 
-// Four keys of a 16-bit [key][d] tile in LDS for one d per lane: sixteen lanes give the addresses of four keys' rows of
-// sixteen values (lane i: row i / 4, values 4 (i % 4) ..), lane i gets value i of the four rows.
-__device__ __forceinline__ u32x2 lds_read_tr(const void* p) {
-  return bitcast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
+// LDS at a byte address.
+__device__ __forceinline__ uint32_t lds_address(const u32x4* p) {
+  return (uint32_t)(uintptr_t)(lds_u32x4*)p;
+}
+__device__ __forceinline__ u32x4 lds_16(uint32_t at) { return *(lds_u32x4*)(uintptr_t)at; }
+// Four keys of a 16-bit [key][d] tile for one d per lane: sixteen lanes give the addresses of four keys' rows of sixteen
+// values (lane i: row i / 4, values 4 (i % 4) ..), lane i gets value i of the four rows.
+__device__ __forceinline__ u32x2 lds_tr(uint32_t at) {
+  return bitcast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at));
+}
+
+// Swizzles (in 16-byte chunks) of the rows of DP values of a tile in LDS.  K: sixteen consecutive rows' chunks of one column fall
+// into different banks.  V: so do the 32-byte pieces of four consecutive rows that a transposing read takes.  Each stays
+// inside aligned spans of 256, 128 or 64 bytes, of which a row is a multiple.
+template <int DP>
+constexpr int kSpanOf = DP % 128 == 0 ? 256 : (DP % 64 == 0 ? 128 : 64);
+template <int DP>
+__device__ __forceinline__ int swizzle_k(int row) {
+  return kSpanOf<DP> == 256 ? row & 15 : (kSpanOf<DP> == 128 ? (row >> 1) & 7 : (row >> 2) & 3);
+}
+template <int DP>
+__device__ __forceinline__ int swizzle_v(int row) {
+  return kSpanOf<DP> == 256 ? (row & 3) << 2 : (kSpanOf<DP> == 128 ? ((row >> 1) & 1) << 2 : 0);
 }
 
 // Partial results in a workspace: (m, l) of every row and part, then O.

@@ -4,9 +4,11 @@
 // take 32 keys at a time, each with a running maximum and sum of its own, and join at the end through LDS.  S^T = K Q^T
 // puts a head into a column (lane & 15), so maxima, sums and rescaling stay in a lane but for two exchanges, and P^T is
 // the right operand of O^T = V^T P^T as it stands, rounded to a high and a low 16-bit part: the cache's bytes bound the
-// kernel, so the second product costs nothing and only the output is rounded.  K goes from the cache into MFMA layout; V
-// has the same layout on arrival and turns in a part of LDS that is the wave's own.  The next keys are on their way
-// while a tile is computed.
+// kernel, so the second product costs nothing and only the output is rounded.
+//
+// Consecutive lanes read consecutive 16 bytes of a token's row, whole 128-byte lines a load and past the caches: in MFMA
+// layout at once (64 bytes of sixteen rows a load) 176 sequences of up to 4096 tokens take 266 us, so 222.  The tile then
+// turns through a part of LDS that is the wave's own.  The next tile's K and V are on their way meanwhile.
 //
 // 16-bit caches are operands as they are, E4M3 codes times a power of two are exact in bf16.
 #include <algorithm>
@@ -19,68 +21,34 @@ namespace {
 
 constexpr int kDecodeWaves = 4, kWaveKeys = 32;
 
+// A wave's tile of K or V on the way: load n has chunk (64 n + lane) of its rows' 16-byte chunks, one row behind another.
 template <int FMT, int DP>
-struct DecodeLoads {  // one tile of K or V as it is stored: lane (r = lane & 15, g = lane >> 4) has rows r and 16 + r
-  static constexpr int N = FMT == MOE_KV_MXFP8 ? DP / 64 : DP / 32;  // 16-byte loads of a row
-  u32x4 q[2][N];
-  uint32_t sc[2][FMT == MOE_KV_MXFP8 ? N : 1];  // MXFP8: scale code of each load's block
-};
-
-// First value of the operand of step st for lanes of group g.
-template <int FMT>
-__device__ __forceinline__ int operand_d(int st, int g) {
-  return FMT == MOE_KV_MXFP8 ? 64 * (st >> 1) + 16 * g + 8 * (st & 1) : 32 * st + 8 * g;
-}
-
-template <int FMT, int DP, bool EXACT>
-__device__ __forceinline__ void load_rows(DecodeLoads<FMT, DP>& t, const void* base, const uint8_t* scales,
-                                          const int64_t (&at)[2], const int64_t (&sat)[2], int g, int D) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int n = 0; n < DecodeLoads<FMT, DP>::N; ++n) {
-      const int d = FMT == MOE_KV_MXFP8 ? 64 * n + 16 * g : 32 * n + 8 * g;
-      t.q[h][n] = u32x4{0, 0, 0, 0};
-      if (EXACT || d < D)
-        t.q[h][n] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>((const char*)base + at[h] + (FMT == MOE_KV_MXFP8 ? d : 2 * d)));
-      if constexpr (FMT == MOE_KV_MXFP8) {
-        t.sc[h][n] = 0;
-        if (EXACT || d < D) t.sc[h][n] = scales[sat[h] + (d >> 5)];
-      }
-    }
-}
-// The operand of step st, row half h.
-template <int FMT, int DP>
-__device__ __forceinline__ u32x4 operand(const DecodeLoads<FMT, DP>& t, int h, int st) {
-  if constexpr (FMT == MOE_KV_MXFP8) {
-    const float s = e8m0_to_f32(t.sc[h][st >> 1]);
-    u32x4 r;
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint32_t c = t.q[h][st >> 1][2 * (st & 1) + w];
-      r[2 * w] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
-      r[2 * w + 1] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
-    }
-    return r;
-  } else {
-    return t.q[h][st];
+struct Rows {
+  static constexpr int CH = FMT == MOE_KV_MXFP8 ? DP / 16 : DP / 8;  // chunks of a row as it is stored
+  static constexpr int N = kWaveKeys * CH / 64;
+  u32x4 q[N];
+  static __device__ __forceinline__ int row(int n, int lane) {
+    return 64 % CH == 0 ? n * (64 / CH) + lane / CH : (64 * n + lane) / CH;
   }
+  static __device__ __forceinline__ int chunk(int n, int lane) { return 64 % CH == 0 ? lane % CH : (64 * n + lane) % CH; }
+};
+__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, lane, kWave), hi = (uint32_t)__shfl((int)(v >> 32), lane, kWave);
+  return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// Place (16-byte chunk) of chunk c of key `row` in a wave's V tile: sixteen rows' chunks of one column fall into
-// different banks on the way in, the 32-byte pieces of four consecutive rows on the way out.
+// E8M0 codes of a row's 32-value blocks.
 template <int DP>
-__device__ __forceinline__ int v_chunk(int row, int c) {
-  if constexpr (DP % 128 == 0) return c ^ (((row & 3) << 1) | ((row >> 2) & 1) | (((row >> 3) & 1) << 3));
-  else return c ^ (((row >> 1) & 1) << 1 | ((row >> 2) & 1) | (((row >> 3) & 1) << 2));
-}
+struct RowScales {
+  uint32_t w[(DP / 32 + 3) / 4];
+};
 
 template <int FMT, int DP, bool EXACT, int PER_SIMD>
 __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(DecodeArgs a) {
-  constexpr bool F16 = FMT == MOE_KV_FP16;
+  constexpr bool F16 = FMT == MOE_KV_FP16, MX = FMT == MOE_KV_MXFP8;
   constexpr int ST = DP / 32, CT = DP / 16, W = kDecodeWaves;
-  __shared__ __attribute__((aligned(16))) u32x4 vt[W][kWaveKeys * DP / 8];  // V tiles; in the end O of the waves
+  typedef Rows<FMT, DP> R;
+  __shared__ __attribute__((aligned(256))) u32x4 tiles[W][kWaveKeys * DP / 8];  // K, then V, of 16 bits; in the end O
   __shared__ float stat[W][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -92,12 +60,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   const int lo = a.window > 0 ? max(0, len - a.window) : 0;
   const int64_t from64 = lo + (int64_t)part * a.part_keys;
   const int from = (int)min(from64, (int64_t)len), to = (int)min(from64 + a.part_keys, (int64_t)len);
-  const int64_t row = (int64_t)b * a.Hq + kvh * a.G + head0 + r;  // this column's output row
-  const bool mine = r < heads;
   const AttnParts parts = attn_parts_dev(a.ws, (int64_t)a.B * a.Hq, a.parts);
-  const int64_t slot = row * a.parts + part;
   if (a.parts > 1 && from >= to) {  // nothing here
-    if (wave == 0 && g == 0 && mine) {
+    if (wave == 0 && g == 0 && r < heads) {
+      const int64_t slot = ((int64_t)b * a.Hq + kvh * a.G + head0 + r) * a.parts + part;
       parts.ml[2 * slot] = -INFINITY;
       parts.ml[2 * slot + 1] = 0.0f;
     }
@@ -109,33 +75,86 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   const uint16_t* qp = a.q + (int64_t)b * a.q_ts + (int64_t)(kvh * a.G + head0 + min(r, heads - 1)) * a.q_hs;
 #pragma unroll
   for (int st = 0; st < ST; ++st) {
-    const int d = operand_d<FMT>(st, g);
+    const int d = 32 * st + 8 * g;
     qf[st] = u32x4{0, 0, 0, 0};
     if (EXACT || d < a.D) qf[st] = ld16(qp + d);
   }
 
-  // Rows of a tile: pages from the table, then byte offsets.  A key past the range or on a page that is none reads the
-  // cache's first row and counts as masked.  Loads return in order, so a tile's pages are asked for before the K and V of
-  // the tile in front of it: their use then waits for neither.
-  int page[2], key[2];
+  // Keys of a tile, one to a lane (twice): page from the table, then byte offset.  A key past the range or on a page that
+  // is none reads the cache's first row and counts as masked.  Loads return in order, so a tile's pages are asked for
+  // before the K and V of the tile in front of it: their use then waits for neither.
+  int page, key;
   const auto look_up = [&](int j0) {
+    key = j0 + (lane & 31);
+    page = table[div_by(a.page_size, (uint32_t)min(key, a.max_len - 1))];
+  };
+  int64_t at, sat;
+  uint32_t seen;  // bit: key of the tile
+  const auto place = [&]() {
+    const bool ok = key < to && (uint32_t)page < (uint32_t)a.n_pages;
+    const int64_t p = ok ? page : 0;
+    const int off = ok ? key - (int)(div_by(a.page_size, (uint32_t)key) * a.page_size.d) : 0;
+    at = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
+    if (!MX) at *= 2;
+    if (MX) sat = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
+    seen = (uint32_t)__builtin_amdgcn_ballot_w64(ok);
+  };
+  const auto load = [&](R& t, const void* base) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      key[h] = j0 + 16 * h + r;
-      page[h] = table[div_by(a.page_size, (uint32_t)min(key[h], a.max_len - 1))];
+    for (int n = 0; n < R::N; ++n) {
+      const int c = R::chunk(n, lane);
+      const char* p = (const char*)base + from_lane(at, R::row(n, lane)) + 16 * c;
+      t.q[n] = u32x4{0, 0, 0, 0};
+      if (EXACT || c * (MX ? 16 : 8) < a.D) t.q[n] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
     }
   };
-  int64_t at[2], sat[2];
-  bool ok[2];
-  const auto place = [&]() {
+  RowScales<DP> sc;  // MXFP8: lanes 0-31 have those of K, lanes 32-63 of V
+  const auto load_scales = [&]() {
+    if constexpr (MX) {
+      const uint8_t* p = (lane < 32 ? a.scale_k : a.scale_v) + sat;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      ok[h] = key[h] < to && (uint32_t)page[h] < (uint32_t)a.n_pages;
-      const int64_t p = ok[h] ? page[h] : 0;
-      const int off = ok[h] ? key[h] - (int)(div_by(a.page_size, (uint32_t)key[h]) * a.page_size.d) : 0;
-      at[h] = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
-      sat[h] = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
-      if (FMT != MOE_KV_MXFP8) at[h] *= 2;
+      for (uint32_t& w : sc.w) w = 0;
+      if constexpr (EXACT) {
+        __builtin_memcpy(sc.w, p, DP / 32);
+      } else {
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i)
+          if (32 * i < a.D) sc.w[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+      }
+    }
+  };
+  // A tile into LDS as 16-bit rows; rows of masked keys as zeros where those are asked for (0 * NaN is no zero).
+  const uint32_t lds0 = lds_address(tiles[wave]);
+  const auto store = [&](const R& t, bool v, uint32_t keep) {
+#pragma unroll
+    for (int n = 0; n < R::N; ++n) {
+      const int row = R::row(n, lane), c = R::chunk(n, lane);
+      const int sw = v ? swizzle_v<DP>(row) : swizzle_k<DP>(row);
+      u32x4 x = t.q[n];
+      if (v && keep != ~0u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = (keep >> row) & 1 ? x[i] : 0u;
+      }
+      u32x4* to_row = &tiles[wave][row * (DP / 8)];
+      if constexpr (MX) {
+        uint32_t code = 0;
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(sc.w) / 4); ++i) {
+          const uint32_t w = (uint32_t)__shfl((int)sc.w[i], row + (v ? 32 : 0), kWave);
+          code = (c >> 3) == i ? (w >> (8 * ((c >> 1) & 3))) & 0xFF : code;
+        }
+        const float s = e8m0_to_f32(v && keep != ~0u && !((keep >> row) & 1) ? 127u : code);
+        u32x4 y[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          y[i >> 1][2 * (i & 1)] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], s, false));
+          y[i >> 1][2 * (i & 1) + 1] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], s, true));
+        }
+        to_row[(2 * c) ^ sw] = y[0];
+        to_row[(2 * c + 1) ^ sw] = y[1];
+      } else {
+        to_row[c ^ sw] = x;
+      }
     }
   };
 
@@ -146,38 +165,44 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   const float c = a.c;
   constexpr int kStep = W * kWaveKeys;
   const int start = from + wave * kWaveKeys;
-  DecodeLoads<FMT, DP> k, v;
-  u32x4* mine_v = vt[wave];
+  R k, v;
+  RowScales<DP> sc_now;
   if (start < to) {
     look_up(start);
     place();
     look_up(start + kStep);
-    load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
-    load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
+    load_scales();
+    load(k, a.cache_k);
+    load(v, a.cache_v);
   }
   for (int j0 = start; j0 < to; j0 += kStep) {
-    const bool now[2] = {ok[0], ok[1]};
+    const uint32_t now = seen;
     const bool more = j0 + kStep < to;
+    store(k, false, now);
+    if constexpr (MX) sc_now = sc;
+    if (more) {
+      place();
+      look_up(j0 + 2 * kStep);
+      load_scales();
+      load(k, a.cache_k);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     f32x4 s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
     for (int st = 0; st < ST; ++st)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) s[h] = mfma_16x16x32<F16>(operand<FMT, DP>(k, h, st), qf[st], s[h]);
-    if (more) {
-      place();
-      look_up(j0 + 2 * kStep);
-      load_rows<FMT, DP, EXACT>(k, a.cache_k, a.scale_k, at, sat, g, a.D);
-    }
+      for (int h = 0; h < 2; ++h)
+        s[h] = mfma_16x16x32<F16>(lds_16(lds0 + (16 * h + r) * (2 * DP) + (((4 * st + g) ^ swizzle_k<DP>(16 * h + r)) << 4)),
+                                  qf[st], s[h]);
     float top = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t seen = (uint32_t)__ballot(now[h]) >> (4 * g);  // (lanes 0-15 hold the sixteen rows' bits)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[h][e] = (seen >> e) & 1 ? s[h][e] : -INFINITY;
+        s[h][e] = (now >> (16 * h + 4 * g + e)) & 1 ? s[h][e] : -INFINITY;
         top = fmaxf(top, s[h][e]);
       }
-    }
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
     top = fmaxf(top, __shfl_xor(top, 32, kWave));
     const float next = fmaxf(m, top);
@@ -199,35 +224,33 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
         ph[2 * h + (e >> 1)] = hi;
         pl[2 * h + (e >> 1)] = pack16<F16>(e0 - unpack16(hi, 0, F16), e1 - unpack16(hi, 1, F16));
       }
-    // V through LDS (rows of masked keys as zeros: 0 * NaN is no zero)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int st = 0; st < ST; ++st) {
-        u32x4 w = operand<FMT, DP>(v, h, st);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] = now[h] ? w[x] : 0u;
-        const int vr = 16 * h + r;
-        mine_v[vr * (DP / 8) + v_chunk<DP>(r, operand_d<FMT>(st, g) >> 3)] = w;
-      }
-    if (more) load_rows<FMT, DP, EXACT>(v, a.cache_v, a.scale_v, at, sat, g, a.D);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (MX) {  // (the next tile's scales are on their way already)
+      const RowScales<DP> next_sc = sc;
+      sc = sc_now;
+      store(v, true, now);
+      sc = next_sc;
+    } else {
+      store(v, true, now);
+    }
+    if (more) load(v, a.cache_v);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const char* vb = reinterpret_cast<const char*>(mine_v);
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       u32x4 w;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int key = 4 * g + (r >> 2), d = 16 * i + 4 * (r & 3);
-        const u32x2 t = lds_read_tr(vb + (16 * h + key) * (2 * DP) + (v_chunk<DP>(key, d >> 3) << 4) + ((d & 7) << 1));
+        const int row = 16 * h + 4 * g + (r >> 2), d = 16 * i + 4 * (r & 3);
+        const u32x2 t = lds_tr(lds0 + row * (2 * DP) + (((d >> 3) ^ swizzle_v<DP>(row)) << 4) + ((d & 7) << 1));
         w[2 * h] = t[0];
         w[2 * h + 1] = t[1];
       }
       o[i] = mfma_16x16x32<F16>(w, pl, o[i]);
       o[i] = mfma_16x16x32<F16>(w, ph, o[i]);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   }
 
@@ -246,22 +269,23 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   for (int w = 0; w < W; ++w)
     sum += stat[w][0][r] == -INFINITY ? stat[w][1][r] : stat[w][1][r] * __builtin_amdgcn_exp2f((stat[w][0][r] - all) * c);
   const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - all) * c);
-  // O of a wave as [16 heads][DP] fp32, in its V tile's place: float 4-groups of a head's row take turns with the head
-  float* ow = reinterpret_cast<float*>(mine_v);
+  // O of a wave as [16 heads][DP] fp32, in its tile's place: float 4-groups of a head's row take turns with the head
+  float* ow = reinterpret_cast<float*>(tiles[wave]);
 #pragma unroll
   for (int i = 0; i < CT; ++i)
     *reinterpret_cast<f32x4*>(ow + r * DP + ((4 * i + g) ^ (r & 7)) * 4) = o[i] * f;
   __syncthreads();
   // thread: head tid / 16, values in groups of four
   const int oh = tid >> 4;
-  const float* o0 = reinterpret_cast<const float*>(&vt[0][0]);
+  const float* o0 = reinterpret_cast<const float*>(&tiles[0][0]);
   const float total = __shfl(sum, oh & 15, kWave), top = __shfl(all, oh & 15, kWave);
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t orow = (int64_t)b * a.Hq + kvh * a.G + head0 + oh;
   if (oh < heads) {
 #pragma unroll
-    for (int u = 0; u < DP / 64; ++u) {
+    for (int u = 0; u < (DP + 63) / 64; ++u) {
       const int q4 = 16 * u + (tid & 15), d = 4 * q4;
+      if (DP % 64 != 0 && d >= DP) continue;
       f32x4 x = {0, 0, 0, 0};
 #pragma unroll
       for (int w = 0; w < W; ++w)
@@ -351,6 +375,7 @@ void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
   (a.D == DP ? decode_kernel<FMT, DP, true, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a)   \
              : decode_kernel<FMT, DP, false, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
   if (a.D <= 64) MOE_DECODE(64, 4);
+  else if (a.D <= 96) MOE_DECODE(96, 2);
   else if (a.D <= 128) MOE_DECODE(128, 2);
   else if (a.D <= 192) MOE_DECODE(192, 2);
   else MOE_DECODE(256, 1);

@@ -20,20 +20,6 @@ namespace {
 
 constexpr int kTileKeys = 64, kPartKeys = 512;
 
-// Swizzles (in 16-byte chunks) of a tile's rows of DP values.  K: sixteen consecutive rows' chunks of one column fall
-// into different banks.  V: so do the 32-byte pieces of four consecutive rows that a transposing read takes.  Each stays
-// inside aligned spans of 256, 128 or 64 bytes, of which a row is a multiple.
-template <int DP>
-constexpr int kSpanOf = DP % 128 == 0 ? 256 : (DP % 64 == 0 ? 128 : 64);
-template <int DP>
-__device__ __forceinline__ int swizzle_k(int row) {
-  return kSpanOf<DP> == 256 ? row & 15 : (kSpanOf<DP> == 128 ? (row >> 1) & 7 : (row >> 2) & 3);
-}
-template <int DP>
-__device__ __forceinline__ int swizzle_v(int row) {
-  return kSpanOf<DP> == 256 ? (row & 3) << 2 : (kSpanOf<DP> == 128 ? ((row >> 1) & 1) << 2 : 0);
-}
-
 __device__ __forceinline__ float other_half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -99,13 +85,6 @@ template <bool F16>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   constexpr uint32_t e = F16 ? 0x7C00u : 0x7F80u;
   return ((w & e) == e ? 0xFFFFu : 0u) | ((w & (e << 16)) == (e << 16) ? 0xFFFF0000u : 0u);
-}
-
-typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) const u32x2 lds_u32x2;
-__device__ __forceinline__ u32x4 lds_16(uint32_t at) { return *(lds_u32x4*)(uintptr_t)at; }
-__device__ __forceinline__ u32x2 lds_tr(uint32_t at) {
-  return bitcast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(uintptr_t)at));
 }
 
 template <bool F16, int DP, bool EXACT, int NW, int PER_SIMD>
@@ -203,7 +182,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 
   // LDS addresses.  A step inside a span is an exclusive-or of a lane's address, one to another span an addition.
   constexpr int kSpan = kSpanOf<DP>, KS = kSpan / 32, VS = kSpan / 64;
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) u32x4*)&lds[0][0][0];
+  const uint32_t lds0 = lds_address(&lds[0][0][0]);
   constexpr uint32_t kTile = BN * CH * 16;
   const uint32_t k_at = lds0 + col * (2 * DP) + ((half ^ swizzle_k<DP>(col)) << 4);
   const int vi = lane & 15, v_row = 4 * half + (vi >> 2);
