@@ -583,7 +583,7 @@ moe_status moe_attention_prompt(const moe_heads *q, const moe_heads *k, const mo
  *   q, y        [B][n_q_heads][head_dim] bf16 (MOE_KV_BF16, MOE_KV_MXFP8) or fp16 (MOE_KV_FP16), 16-byte aligned, strides
  *               multiples of 8 values
  *   page_table  [B] rows of table_width int32, table_stride apart;  lens [B] int32
- *   max_len     at most table_width * page_size; the work is shared out by it, so it should be near the longest row
+ *   max_len     at most table_width * page_size and 2^30; the work is shared out by it, so it should be near the longest row
  *   lse         [B][n_q_heads] fp32, or NULL
  *   workspace   moe_attention_decode_workspace_bytes(...) bytes, 16-byte aligned (NULL if that is 0)
  * Errors: NULL, SHAPE (B<0, B * n_q_heads > 2^23, heads, head_dim, strides, max_len, scale, window<0), BLOCK, DTYPE,

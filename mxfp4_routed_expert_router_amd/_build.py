@@ -24,9 +24,8 @@ HIPCC_FLAGS = [
 # Flags of single sources.  The attention loops have rare branches that a whole wave takes together; left to itself the
 # compiler rewrites them as if lanes could part there, and keeps two copies of the accumulators for it (a prompt's loop:
 # 256 registers and 64 moves a tile, 184 and none with the flag).
-SOURCE_FLAGS = {
-    "attn_prompt.hip": ["-mllvm", "-structurizecfg-skip-uniform-regions"],
-}
+_WAVE_BRANCHES = ["-mllvm", "-structurizecfg-skip-uniform-regions"]
+SOURCE_FLAGS = {"attn_prompt.hip": _WAVE_BRANCHES, "attn_decode.hip": _WAVE_BRANCHES}
 
 
 def hipcc() -> str:

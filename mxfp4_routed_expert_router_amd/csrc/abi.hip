@@ -1014,7 +1014,7 @@ moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const mo
 }
 
 size_t moe_attention_decode_workspace_bytes(int B, int n_q_heads, int n_kv_heads, int head_dim, int max_len) {
-  if (B <= 0 || max_len <= 0 || check_head_counts(n_q_heads, n_kv_heads, head_dim) != MOE_OK) return 0;
+  if (B <= 0 || max_len <= 0 || max_len > 1 << 30 || check_head_counts(n_q_heads, n_kv_heads, head_dim) != MOE_OK) return 0;
   return round_up(moe::decode_workspace_bytes(B, n_q_heads, n_kv_heads, head_dim, max_len), 256);
 }
 
@@ -1032,7 +1032,7 @@ moe_status moe_attention_decode(const moe_heads* q, int B, int n_q_heads, const 
   const int dt = cache->fmt == MOE_KV_FP16 ? MOE_DT_FP16 : MOE_DT_BF16;
   if (q->dtype != dt || y->dtype != dt) return MOE_ERR_DTYPE;
   if ((st = check_heads(*q, 8)) != MOE_OK || (st = check_heads(*y, 8)) != MOE_OK) return st;
-  if (!usable_scale(scale) || window < 0 || max_len < 0 || table_width < 0 ||
+  if (!usable_scale(scale) || window < 0 || max_len < 0 || max_len > 1 << 30 || table_width < 0 ||
       max_len > (int64_t)table_width * cache->page_size || table_stride < 0 || table_stride > kMostStride)
     return MOE_ERR_SHAPE;
   if ((int64_t)B * n_q_heads > kMostBlocks) return MOE_ERR_SHAPE;

@@ -64,6 +64,9 @@ __device__ __forceinline__ int swizzle_v(int row) {
   return kSpanOf<DP> == 256 ? (row & 3) << 2 : (kSpanOf<DP> == 128 ? ((row >> 1) & 1) << 2 : 0);
 }
 
+// (a ballot is uniform to the compiler, __any() is not: its branches would keep both sides' values in registers)
+__device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
+
 // Partial results in a workspace: (m, l) of every row and part, then O.
 struct AttnParts {
   float* ml;  // [rows][parts][2]

@@ -43,7 +43,9 @@ struct RowScales {
   uint32_t w[(DP / 32 + 3) / 4];
 };
 
-template <int FMT, int DP, bool EXACT, int PER_SIMD>
+// WHOLE: pages are multiples of a tile's 32 keys, so that a tile lies on one page and its addresses are scalars but for a
+// lane's place in it; else each key has its own.
+template <int FMT, int DP, bool EXACT, bool WHOLE, int PER_SIMD>
 __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(DecodeArgs a) {
   constexpr bool F16 = FMT == MOE_KV_FP16, MX = FMT == MOE_KV_MXFP8;
   constexpr int ST = DP / 32, CT = DP / 16, W = kDecodeWaves;
@@ -58,7 +60,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   const int kvh = in / m_tiles, head0 = (in - kvh * m_tiles) * 16, heads = min(16, a.G - head0);
   const int len = min(max(a.lens[b], 0), a.max_len);
   const int lo = a.window > 0 ? max(0, len - a.window) : 0;
-  const int64_t from64 = lo + (int64_t)part * a.part_keys;
+  // (tiles start at multiples of 32 keys; those in front of the window are masked)
+  const int64_t from64 = lo / kWaveKeys * kWaveKeys + (int64_t)part * a.part_keys;
   const int from = (int)min(from64, (int64_t)len), to = (int)min(from64 + a.part_keys, (int64_t)len);
   const AttnParts parts = attn_parts_dev(a.ws, (int64_t)a.B * a.Hq, a.parts);
   if (a.parts > 1 && from >= to) {  // nothing here
@@ -80,30 +83,58 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     if (EXACT || d < a.D) qf[st] = ld16(qp + d);
   }
 
-  // Keys of a tile, one to a lane (twice): page from the table, then byte offset.  A key past the range or on a page that
-  // is none reads the cache's first row and counts as masked.  Loads return in order, so a tile's pages are asked for
-  // before the K and V of the tile in front of it: their use then waits for neither.
+  // Where a tile's rows are.  A key past the range or on a page that is none counts as masked; its row is read from the
+  // cache's first page.
+  //   WHOLE: 64 tiles' pages are loaded at once, one to a lane, and a tile's is read from its lane.
+  //   Else a tile's keys are one to a lane (twice), with page and byte offset.  Loads return in order, so a tile's pages are
+  // asked for before the K and V of the tile in front of it: their use then waits for neither.
+  constexpr int kStep = W * kWaveKeys;
+  const int start = from + wave * kWaveKeys;
   int page, key;
   const auto look_up = [&](int j0) {
-    key = j0 + (lane & 31);
-    page = table[div_by(a.page_size, (uint32_t)min(key, a.max_len - 1))];
+    if constexpr (WHOLE) {
+      if (((j0 - start) / kStep & 63) == 0)
+        page = table[div_by(a.page_size, (uint32_t)min(j0 + lane * kStep, a.max_len - 1))];
+    } else {
+      key = j0 + (lane & 31);
+      page = table[div_by(a.page_size, (uint32_t)min(key, a.max_len - 1))];
+    }
   };
   int64_t at, sat;
   uint32_t seen;  // bit: key of the tile
-  const auto place = [&]() {
-    const bool ok = key < to && (uint32_t)page < (uint32_t)a.n_pages;
-    const int64_t p = ok ? page : 0;
-    const int off = ok ? key - (int)(div_by(a.page_size, (uint32_t)key) * a.page_size.d) : 0;
-    at = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
+  const auto place = [&](int j0) {
+    if constexpr (WHOLE) {
+      const int of = __builtin_amdgcn_readlane(page, (j0 - start) / kStep & 63);
+      const bool ok = (uint32_t)of < (uint32_t)a.n_pages;
+      const int64_t p = ok ? of : 0;
+      const int off = j0 - (int)(div_by(a.page_size, (uint32_t)j0) * a.page_size.d);
+      at = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
+      sat = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
+      seen = to - j0 >= 32 ? ~0u : (1u << (to - j0)) - 1;
+      if (lo > j0) seen &= ~0u << (lo - j0);  // (lo < j0 + 32)
+      if (!ok) seen = 0;
+    } else {
+      const bool ok = key < to && key >= lo && (uint32_t)page < (uint32_t)a.n_pages;
+      const int64_t p = ok ? page : 0;
+      const int off = ok ? key - (int)(div_by(a.page_size, (uint32_t)key) * a.page_size.d) : 0;
+      at = p * a.c_page + (int64_t)off * a.c_token + (int64_t)kvh * a.c_head;
+      sat = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
+      seen = (uint32_t)__builtin_amdgcn_ballot_w64(ok);
+    }
     if (!MX) at *= 2;
-    if (MX) sat = p * a.s_page + (int64_t)off * a.s_token + (int64_t)kvh * a.s_head;
-    seen = (uint32_t)__builtin_amdgcn_ballot_w64(ok);
   };
+  const uint32_t token = (uint32_t)a.c_token * (MX ? 1 : 2);  // bytes (WHOLE: below 2^24 values)
   const auto load = [&](R& t, const void* base) {
 #pragma unroll
     for (int n = 0; n < R::N; ++n) {
       const int c = R::chunk(n, lane);
-      const char* p = (const char*)base + from_lane(at, R::row(n, lane)) + 16 * c;
+      const char* p;
+      if constexpr (WHOLE && 64 % R::CH == 0)
+        p = (const char*)base + at + n * (64 / R::CH) * (int64_t)token + ((uint32_t)R::row(0, lane) * token + 16 * c);
+      else if constexpr (WHOLE)
+        p = (const char*)base + at + ((uint32_t)R::row(n, lane) * token + 16 * c);
+      else
+        p = (const char*)base + from_lane(at, R::row(n, lane)) + 16 * c;
       t.q[n] = u32x4{0, 0, 0, 0};
       if (EXACT || c * (MX ? 16 : 8) < a.D) t.q[n] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
     }
@@ -111,7 +142,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   RowScales<DP> sc;  // MXFP8: lanes 0-31 have those of K, lanes 32-63 of V
   const auto load_scales = [&]() {
     if constexpr (MX) {
-      const uint8_t* p = (lane < 32 ? a.scale_k : a.scale_v) + sat;
+      const uint8_t* p = (lane < 32 ? a.scale_k : a.scale_v) + sat + (WHOLE ? (int64_t)(lane & 31) * a.s_token : 0);
 #pragma unroll
       for (uint32_t& w : sc.w) w = 0;
       if constexpr (EXACT) {
@@ -163,13 +194,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   for (int i = 0; i < CT; ++i) o[i] = f32x4{0, 0, 0, 0};
   float m = -INFINITY, l = 0.0f;
   const float c = a.c;
-  constexpr int kStep = W * kWaveKeys;
-  const int start = from + wave * kWaveKeys;
   R k, v;
   RowScales<DP> sc_now;
   if (start < to) {
     look_up(start);
-    place();
+    place(start);
     look_up(start + kStep);
     load_scales();
     load(k, a.cache_k);
@@ -181,7 +210,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     store(k, false, now);
     if constexpr (MX) sc_now = sc;
     if (more) {
-      place();
+      place(j0 + kStep);
       look_up(j0 + 2 * kStep);
       load_scales();
       load(k, a.cache_k);
@@ -195,30 +224,38 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
       for (int h = 0; h < 2; ++h)
         s[h] = mfma_16x16x32<F16>(lds_16(lds0 + (16 * h + r) * (2 * DP) + (((4 * st + g) ^ swizzle_k<DP>(16 * h + r)) << 4)),
                                   qf[st], s[h]);
+    // m: reference of the exponents (base 2, scaled).  It rises only when some head's maximum passes it by more than 2^8.
+    const float base = m == -INFINITY ? 0.0f : m;
     float top = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
+        s[h][e] = __builtin_fmaf(s[h][e], c, -base);
         s[h][e] = (now >> (16 * h + 4 * g + e)) & 1 ? s[h][e] : -INFINITY;
         top = fmaxf(top, s[h][e]);
       }
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
     top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    const float next = fmaxf(m, top);
-    const float f = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - next) * c);
-    const float base = next == -INFINITY ? 0.0f : next * c;
-    m = next;
-    l *= f;
+    if (__builtin_expect(wave_any((top > 8.0f) | ((m == -INFINITY) & (top > -INFINITY))), 0)) {
+      float up = m == -INFINITY ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
+      asm volatile("" : "+v"(up));  // (nothing of this rare block ahead of its branch)
+      const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up);  // (O and l are zero before the first key)
+      m = m == -INFINITY ? top : m + up;
+      l *= f;
 #pragma unroll
-    for (int i = 0; i < CT; ++i) o[i] *= f;
+      for (int i = 0; i < CT; ++i) o[i] *= f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[h][e] -= up;
+    }
     u32x4 ph, pl;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e], c, -base));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[h][e + 1], c, -base));
+        const float e0 = __builtin_amdgcn_exp2f(s[h][e]), e1 = __builtin_amdgcn_exp2f(s[h][e + 1]);
         l += e0 + e1;
         const uint32_t hi = pack16<F16>(e0, e1);
         ph[2 * h + (e >> 1)] = hi;
@@ -267,8 +304,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   for (int w = 0; w < W; ++w) all = fmaxf(all, stat[w][0][r]);
 #pragma unroll
   for (int w = 0; w < W; ++w)
-    sum += stat[w][0][r] == -INFINITY ? stat[w][1][r] : stat[w][1][r] * __builtin_amdgcn_exp2f((stat[w][0][r] - all) * c);
-  const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - all) * c);
+    sum += stat[w][0][r] == -INFINITY ? stat[w][1][r] : stat[w][1][r] * __builtin_amdgcn_exp2f(stat[w][0][r] - all);
+  const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - all);
   // O of a wave as [16 heads][DP] fp32, in its tile's place: float 4-groups of a head's row take turns with the head
   float* ow = reinterpret_cast<float*>(tiles[wave]);
 #pragma unroll
@@ -300,10 +337,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     }
     if ((tid & 15) == 0) {
       if (a.parts > 1) {
-        parts.ml[2 * (orow * a.parts + part)] = top * c;
+        parts.ml[2 * (orow * a.parts + part)] = top;
         parts.ml[2 * (orow * a.parts + part) + 1] = total;
       } else if (a.lse) {
-        a.lse[orow] = total == 0.0f ? -INFINITY : (top * c + __builtin_amdgcn_logf(total)) * kLn2;
+        a.lse[orow] = total == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(total)) * kLn2;
       }
     }
   }
@@ -371,15 +408,18 @@ DecodePlan plan_decode(int B, int Hq, int Hkv, int D, int max_len) {
 
 template <int FMT>
 void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
-#define MOE_DECODE(DP, OCC)                                                                \
-  (a.D == DP ? decode_kernel<FMT, DP, true, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a)   \
-             : decode_kernel<FMT, DP, false, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
+#define MOE_DECODE_W(DP, WHOLE, OCC)                                                              \
+  (a.D == DP ? decode_kernel<FMT, DP, true, WHOLE, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a)   \
+             : decode_kernel<FMT, DP, false, WHOLE, OCC><<<g, 64 * kDecodeWaves, 0, stream>>>(a))
+#define MOE_DECODE(DP, OCC) (whole ? MOE_DECODE_W(DP, true, OCC) : MOE_DECODE_W(DP, false, OCC))
+  const bool whole = a.page_size.d % kWaveKeys == 0 && a.c_token < 1 << 24;
   if (a.D <= 64) MOE_DECODE(64, 4);
   else if (a.D <= 96) MOE_DECODE(96, 2);
   else if (a.D <= 128) MOE_DECODE(128, 2);
   else if (a.D <= 192) MOE_DECODE(192, 2);
   else MOE_DECODE(256, 1);
 #undef MOE_DECODE
+#undef MOE_DECODE_W
 }
 
 }  // namespace

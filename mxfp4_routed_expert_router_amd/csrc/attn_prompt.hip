@@ -29,9 +29,6 @@ __device__ __forceinline__ float other_half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// (a ballot is uniform to the compiler, __any() is not: its branches would keep both sides' values in registers)
-__device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
-
 // Next in a block's order: READS LDS reads; a matrix product with TRANS exponentials, VALU vector instructions and READS
 // LDS reads behind it.
 template <int READS>

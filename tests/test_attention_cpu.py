@@ -122,7 +122,7 @@ def test_decode_refusals(fmt):
                 dict(table=None), dict(lens=None)):
         assert f(**bad) == NULL, bad
     for bad in (dict(B=-1), dict(nq=0), dict(nq=3), dict(nq=1026), dict(ts=-1), dict(ts=1 << 41), dict(width=-1),
-                dict(max_len=161), dict(max_len=-1), dict(scale=0.0), dict(scale=math.nan), dict(window=-1),
+                dict(max_len=161), dict(max_len=-1), dict(max_len=(1 << 30) + 1, width=1 << 28), dict(scale=0.0), dict(scale=math.nan), dict(window=-1),
                 dict(B=1 << 22, nq=4), dict(q=heads(dt=dt, ts=-8)), dict(y=heads(dt=dt, hs=-8))):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(q=heads(dt=FP32)), dict(y=heads(dt=FP32)), dict(q=heads(dt=1 - dt)), dict(y=heads(dt=1 - dt))):
