@@ -392,18 +392,25 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnJoin a) {
 struct DecodePlan {
   int parts, part_keys;
 };
-DecodePlan plan_decode(int B, int Hq, int Hkv, int D, int max_len) {
+// Parts of a row of up to n keys (in a window: of what it can touch).  Few rows: 512 workgroups, of one step of their waves
+// at least (one sequence of 777 tokens: 8.7 us; two steps 9.6).  Up to 1024 units of row and head: 3072 workgroups of two
+// steps at least, which evens out rows of different lengths (us for 64 sequences of up to 8192: 1024 workgroups 245, 2048
+// 243, 3072 220, 6144 220; 16 of up to 16384 in MXFP8 82, 74, 74, 78; 8 of 4096 in steps of 128 29.6, of 256 27.7).  More
+// units are even enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long.
+int64_t most_parts(int64_t units, int64_t n) {
   constexpr int kBlockKeys = kDecodeWaves * kWaveKeys;
-  const int64_t units = (int64_t)B * Hkv * ((Hq / Hkv + 15) / 16);
-  int64_t parts = (1024 + units - 1) / units;
-  const int64_t most = (max_len + kBlockKeys - 1) / kBlockKeys;
-  parts = std::max<int64_t>(1, std::min(parts, most));
-  DecodePlan p;
-  const int64_t keys = (max_len + parts - 1) / parts;
-  p.part_keys = (int)((keys + kBlockKeys - 1) / kBlockKeys * kBlockKeys);
-  p.part_keys = std::max(p.part_keys, kBlockKeys);
-  p.parts = (int)std::max<int64_t>(1, (max_len + (int64_t)p.part_keys - 1) / p.part_keys);
-  return p;
+  const int64_t some = std::min((512 + units - 1) / units, (n + kBlockKeys - 1) / kBlockKeys);
+  const int64_t more = units < 1024 ? std::min((3072 + units - 1) / units, n / (2 * kBlockKeys))
+                                    : std::min<int64_t>(16, n / 8192);
+  return std::max<int64_t>(1, std::max(some, more));
+}
+int64_t decode_units(int B, int Hq, int Hkv) { return (int64_t)B * Hkv * ((Hq / Hkv + 15) / 16); }
+DecodePlan plan_decode(const DecodeArgs& a) {
+  constexpr int kBlockKeys = kDecodeWaves * kWaveKeys;
+  const int64_t n = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + kWaveKeys - 1) : a.max_len;
+  const int64_t parts = most_parts(decode_units(a.B, a.Hq, a.Hkv), n);
+  const int64_t keys = std::max<int64_t>(1, ((n + parts - 1) / parts + kBlockKeys - 1) / kBlockKeys) * kBlockKeys;
+  return DecodePlan{(int)std::max<int64_t>(1, (n + keys - 1) / keys), (int)keys};
 }
 
 template <int FMT>
@@ -425,7 +432,7 @@ void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
 }  // namespace
 
 size_t decode_workspace_bytes(int B, int Hq, int Hkv, int D, int max_len) {
-  return attn_parts_bytes((int64_t)B * Hq, plan_decode(B, Hq, Hkv, D, max_len).parts, D);
+  return attn_parts_bytes((int64_t)B * Hq, (int)most_parts(decode_units(B, Hq, Hkv), max_len), D);
 }
 
 hipError_t launch_attn_join(const AttnJoin& j, hipStream_t stream) {
@@ -437,7 +444,7 @@ hipError_t launch_attn_join(const AttnJoin& j, hipStream_t stream) {
 }
 
 hipError_t launch_decode(DecodeArgs a, hipStream_t stream) {
-  const DecodePlan p = plan_decode(a.B, a.Hq, a.Hkv, a.D, a.max_len);
+  const DecodePlan p = plan_decode(a);
   a.parts = p.parts;
   a.part_keys = p.part_keys;
   const dim3 g((unsigned)((int64_t)a.B * p.parts * a.Hkv * ((a.G + 15) / 16)));
