@@ -950,7 +950,6 @@ moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T,
     a.in[i] = heads_dev(in[i]);
     a.out[i] = heads_dev(out[i]);
   }
-  a.n_rows = moe::fast_div((uint32_t)(n_q_heads + 2 * n_kv_heads));
   return hip_status(moe::launch_rope(a, (hipStream_t)stream));
 }
 

@@ -187,8 +187,9 @@ struct RopeArgs {
   uint8_t *scale_k, *scale_v;
   int64_t c_page, c_head, c_token, s_page, s_head, s_token;
   FastDiv page_size;
-  FastDiv n_rows;             // Hq + 2 Hkv
-  int runs, rows_per_wave;    // set by the launch
+  // set by the launch: runs of eight values of a head, heads of a wave, waves of a token's q, of its k (and v), of all
+  int runs, rows_per_wave, q_groups, kv_groups;
+  FastDiv groups;
 };
 hipError_t launch_rope(RopeArgs a, hipStream_t stream);
 

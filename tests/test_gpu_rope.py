@@ -195,3 +195,16 @@ def test_zero_values():
     for t in cache.tensors:
         got = t.cpu()[pg, :, of]
         assert bool(((got == 0) | (got == 128)).all() if t.shape[3] == 64 else (got == 0).all())
+
+
+def test_more_tokens_than_a_launch():
+    """Two launches: tokens around the seam and at the end."""
+    T = (1 << 24) + 37
+    k = torch.randn(T, 1, 8, device=DEV).bfloat16()
+    cos, sin = ref.angles(N, 8)
+    rope = moe.Rope(cos.to(DEV), sin.to(DEV))
+    pos = (torch.arange(T, device=DEV) % N).int()
+    _, got, _ = moe.moe_rope_cache(None, k, None, rope, pos)
+    for at in (slice(0, 50), slice((1 << 24) - 50, (1 << 24) + 37)):
+        _, want, _ = moe.moe_rope_cache(None, k[at].clone(), None, rope, pos[at].clone())
+        assert torch.equal(got[at], want)
