@@ -18,7 +18,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kTileKeys = 64, kPartKeys = 512;
+constexpr int kTileKeys = 64;
 
 __device__ __forceinline__ float other_half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -52,10 +52,12 @@ __device__ __forceinline__ Piece find_piece(const PromptArgs& a, int slot, int r
   const int lane = threadIdx.x & 63;
   for (int b0 = 0; b0 < a.n_seqs; b0 += 64) {
     const int b = b0 + lane;
-    int q0 = 0, q1 = 0;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
     if (b < a.n_seqs) {
       q0 = min(max(a.cu_q[b], 0), a.Tq);
       q1 = min(max(a.cu_q[b + 1], q0), a.Tq);
+      k0 = min(max(a.cu_k[b], 0), a.Tk);
+      k1 = min(max(a.cu_k[b + 1], k0), a.Tk);
     }
     const int tiles = (int)(((int64_t)(q1 - q0) * a.G.d + rows - 1) / rows);
     const int incl = (int)wave_incl_scan_dpp((uint32_t)tiles);
@@ -66,10 +68,8 @@ __device__ __forceinline__ Piece find_piece(const PromptArgs& a, int slot, int r
       p.q0 = __builtin_amdgcn_readlane(q0, s);
       p.nq = __builtin_amdgcn_readlane(q1, s) - p.q0;
       p.tile = __builtin_amdgcn_readlane(incl, s) - 1 - slot;
-      p.k0 = min(max(a.cu_k[b0 + s], 0), a.Tk);
-      p.nk = min(max(a.cu_k[b0 + s + 1], p.k0), a.Tk) - p.k0;
-      p.k0 = __builtin_amdgcn_readfirstlane(p.k0);
-      p.nk = __builtin_amdgcn_readfirstlane(p.nk);
+      p.k0 = __builtin_amdgcn_readlane(k0, s);
+      p.nk = __builtin_amdgcn_readlane(k1, s) - p.k0;
       return p;
     }
     slot -= __builtin_amdgcn_readlane(incl, 63);
@@ -77,6 +77,7 @@ __device__ __forceinline__ Piece find_piece(const PromptArgs& a, int slot, int r
   return Piece{0, 0, 0, 0, -1};
 }
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 // The 16-bit values of a dword that are infinite or NaN, as a mask.
 template <bool F16>
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
@@ -229,13 +230,14 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     // 0 * infinity is no zero: a masked key's value must not reach a row, so values that are not finite go by themselves
     bool wild = false;
     if (__builtin_expect(masked, 0)) {
-      uint32_t bad = 0;
+      u16x2 most = {0, 0};  // of the values' bits without the sign
 #pragma unroll
       for (int u = 0; u < BN * CH / 64; ++u) {
         const u32x4 w = lds_16(lds0 + buf + kTile + (64 * u + lane) * 16);
-        bad |= not_finite<F16>(w[0]) | not_finite<F16>(w[1]) | not_finite<F16>(w[2]) | not_finite<F16>(w[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) most = __builtin_elementwise_max(most, bitcast<u16x2>(w[i] & 0x7FFF7FFFu));
       }
-      wild = wave_any(bad != 0);
+      wild = wave_any(std::max<uint16_t>(most[0], most[1]) >= (F16 ? 0x7C00 : 0x7F80));
     }
     const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
@@ -425,6 +427,11 @@ void launch_exact(const PromptArgs& a, dim3 g, hipStream_t stream) {
   else prompt_kernel<F16, DP, false, NW, PER_SIMD><<<g, 64 * NW, 0, stream>>>(a);
 }
 
+// Keys are shared where a prompt's tiles are too few for the card.  The parts' results cost their bytes twice and a second
+// launch, so the number is the one of least estimated time: rounds of workgroups, tiles of each, and the joining (us, at
+// heads of 128: a tile takes 1.6 alone on its SIMDs and 1.9 with another, 4 for a workgroup's start and end, 4 for a launch;
+// parts' bytes move at 4 TB/s).  A sequence's keys are not known here: twice the mean, at most all.
+// Measured, parts of 1 / 8: 128 tokens behind 16000 (64 heads on 8) 340 / 86 us; 301 tokens 13.6 in one part, 35 in three.
 struct PromptPlan {
   int waves;  // of a workgroup, 32 rows each
   int64_t slots;
@@ -434,12 +441,28 @@ PromptPlan plan_prompt(int Tq, int Tk, int n_seqs, int Hq, int Hkv, int D) {
   PromptPlan p;
   p.waves = 4;
   const int rows = 32 * p.waves;
-  p.slots = ((int64_t)Tq * (Hq / Hkv) + rows - 1) / rows + n_seqs;
-  // Keys are shared where tiles are few: at least 512 keys a part, parts for 512 workgroups
-  const int64_t blocks = p.slots * Hkv, most = (Tk + kPartKeys - 1) / kPartKeys;
-  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((512 + blocks - 1) / blocks, most));
-  p.part_keys = std::max<int64_t>(1, ((Tk + parts - 1) / parts + kTileKeys - 1) / kTileKeys) * kTileKeys;
-  p.parts = (int)std::max<int64_t>(1, ((int64_t)Tk + p.part_keys - 1) / p.part_keys);
+  const int64_t tiles = ((int64_t)Tq * (Hq / Hkv) + rows - 1) / rows, all_rows = (int64_t)Tq * Hq;
+  p.slots = tiles + n_seqs;
+  p.parts = 1;
+  p.part_keys = std::max(1, (Tk + kTileKeys - 1) / kTileKeys) * kTileKeys;
+  const int64_t blocks = std::max<int64_t>(tiles, std::min(n_seqs, Tq)) * Hkv;
+  const int at_once = 256 * (D <= 64 ? 4 : (D <= 128 ? 2 : 1));
+  if (blocks >= at_once / 2) return p;
+  const double keys = std::min<double>(Tk, 2.0 * Tk / n_seqs);
+  double best = 0.0;
+  for (const int n : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+    const int64_t part = ((int64_t)(keys / n) + kTileKeys) / kTileKeys * kTileKeys;
+    const int64_t parts = n == 1 ? 1 : (Tk + part - 1) / part;
+    if (n > 1 && (parts < 2 || parts > 1024 || attn_parts_bytes(all_rows, (int)parts, D) > (size_t)256 << 20)) continue;
+    const double rounds = (double)((blocks * n + at_once - 1) / at_once);
+    const double tile = (blocks * n > 256 ? 1.9 : 1.6) * D / 128;
+    const double us = rounds * ((double)part / kTileKeys * tile + 4) + (n > 1 ? 4 + (double)all_rows * n * (D + 2) * 8 / 4e6 : 0);
+    if (n == 1 || us < 0.9 * best) {
+      best = us;
+      p.parts = (int)parts;
+      if (n > 1) p.part_keys = (int)part;
+    }
+  }
   return p;
 }
 
