@@ -28,6 +28,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -827,20 +828,36 @@ def moe_linear(x: torch.Tensor, W: LinearWeights, bias: Optional[torch.Tensor] =
 
 # ----------------------------------------------------------------------------------------------------
 # Attention
-def _heads(what: str, t: torch.Tensor, shape, index: int) -> moe_heads:
-    """Description of a tensor [tokens][heads][head_dim] with contiguous heads on GPU `index` (-1: the CPU)."""
-    if t.shape != shape or t.get_device() != index:
-        raise ValueError(f"{what} must be {tuple(shape)} on GPU {index}, got {tuple(t.shape)} on {t.device}")
-    ts, hs, ds = t.stride()
-    if ds != 1 and shape[2] > 1:
-        raise ValueError(f"{what}: a head's values must be contiguous, got strides {t.stride()}")
-    return moe_heads(t.data_ptr(), _dtype(what, t), ts if shape[0] > 1 else shape[1] * shape[2],
-                     hs if shape[1] > 1 else shape[2])
+def _heads(what: str, t: torch.Tensor, shape, index: int) -> tuple:
+    """Fields of a moe_heads: a tensor [tokens][heads][head_dim] with contiguous heads on GPU `index` (-1: the CPU)."""
+    if t.shape == shape and t.get_device() == index:
+        ts, hs, ds = t.stride()
+        if ds == 1 or shape[2] <= 1:
+            dt = DTYPES.get(t.dtype)
+            if dt is None:
+                raise TypeError(f"{what} must be bfloat16, float16 or float32, got {t.dtype}")
+            return (t.data_ptr(), dt, ts if shape[0] > 1 else shape[1] * shape[2], hs if shape[1] > 1 else shape[2])
+    raise ValueError(f"{what} must be {tuple(shape)} with contiguous heads on GPU {index}, got {tuple(t.shape)} with strides "
+                     f"{t.stride()} on {t.device}")
+
+
+_HEADS_BYTES = ctypes.sizeof(moe_heads)
+_HEADS_PACKED = {n: (struct.Struct("@" + "Pi4xqq" * n), ctypes.c_char * (n * _HEADS_BYTES)) for n in (2, 4, 6)}
+_NO_HEADS = (0, 0, 0, 0)
+
+
+def _packed(fields: tuple, n: int):
+    """n moe_heads behind one another, from their fields: one object instead of n (which a call of few microseconds
+    would feel).  The caller keeps it until its call is made."""
+    pack, kind = _HEADS_PACKED[n]
+    return kind.from_buffer_copy(pack.pack(*fields))
 
 
 def _ints(what: str, t: torch.Tensor, shape, index: int) -> int:
-    _dense(what, t, torch.int32, shape, index)
-    return t.data_ptr()
+    if t.dtype is torch.int32 and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on GPU {index}, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}")
 
 
 class Rope:
@@ -929,15 +946,24 @@ def moe_rope_cache(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
         act = torch.bfloat16 if cache is None else cache.act
         out = tuple(None if t is None else torch.empty((T, n, D), dtype=act, device=x.device)
                     for t, n in ((q, nq), (k, nkv), (v if k is not None else None, nkv)))
-    described = [None if t is None else _heads(f"moe_rope_cache: {name}", t, (T, n, D), gpu)
-                 for name, t, n in (("q", q, nq), ("k", k, nkv), ("v", v, nkv), ("q_out", out[0], nq),
-                                    ("k_out", out[1], nkv), ("v_out", out[2], nkv))]
+    q_out, k_out, v_out = out
+    qs, ks = (T, nq, D), (T, nkv, D)
+    none = _NO_HEADS
+    h = _packed((none if q is None else _heads("moe_rope_cache: q", q, qs, gpu))
+                + (none if k is None else _heads("moe_rope_cache: k", k, ks, gpu))
+                + (none if v is None else _heads("moe_rope_cache: v", v, ks, gpu))
+                + (none if q_out is None else _heads("moe_rope_cache: q_out", q_out, qs, gpu))
+                + (none if k_out is None else _heads("moe_rope_cache: k_out", k_out, ks, gpu))
+                + (none if v_out is None else _heads("moe_rope_cache: v_out", v_out, ks, gpu)), 6)
     if rope is not None and rope.index != gpu or cache is not None and cache.index != gpu:
         raise ValueError(f"moe_rope_cache: the rope and the cache must be on GPU {gpu}")
-    pos = None if positions is None else _ints("moe_rope_cache: positions", positions, (T,), gpu)
-    sl = None if slots is None else _ints("moe_rope_cache: slots", slots, (T,), gpu)
-    _enqueue("moe_rope_cache", gpu, None if rope is None else rope.at, pos, T, nq, nkv, D,
-             *(None if h is None else ctypes.addressof(h) for h in described), None if cache is None else cache.at, sl)
+    at, n = ctypes.addressof(h), _HEADS_BYTES
+    _enqueue("moe_rope_cache", gpu, None if rope is None else rope.at,
+             None if positions is None else _ints("moe_rope_cache: positions", positions, (T,), gpu), T, nq, nkv, D,
+             None if q is None else at, None if k is None else at + n, None if v is None else at + 2 * n,
+             None if q_out is None else at + 3 * n, None if k_out is None else at + 4 * n,
+             None if v_out is None else at + 5 * n, None if cache is None else cache.at,
+             None if slots is None else _ints("moe_rope_cache: slots", slots, (T,), gpu))
     return out
 
 
@@ -971,6 +997,7 @@ def moe_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
     kh = _heads("moe_attention_prompt: k", k, (Tk, nkv, D), gpu)
     vh = _heads("moe_attention_prompt: v", v, (Tk, nkv, D), gpu)
     y, lse, yh = _attention_out("moe_attention_prompt", q, out, want_lse, gpu)
+    h = _packed(qh + kh + vh + yh, 4)
     cq = _ints("moe_attention_prompt: cu_q", cu_q, (n + 1,), gpu)
     ck = cq if cu_k is None else _ints("moe_attention_prompt: cu_k", cu_k, (n + 1,), gpu)
     ws = workspace
@@ -978,9 +1005,9 @@ def moe_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
         ws = _workspace(moe_attention_prompt_workspace_bytes(Tq, Tk, n, nq, nkv, D), q.device)
     else:
         _on_gpu("moe_attention_prompt: workspace", ws, gpu)
-    at = ctypes.addressof
-    _enqueue("moe_attention_prompt", gpu, at(qh), at(kh), at(vh), cq, ck, n, Tq, Tk, nq, nkv, D,
-             D ** -0.5 if scale is None else scale, int(bool(causal)), window, at(yh),
+    at, size = ctypes.addressof(h), _HEADS_BYTES
+    _enqueue("moe_attention_prompt", gpu, at, at + size, at + 2 * size, cq, ck, n, Tq, Tk, nq, nkv, D,
+             D ** -0.5 if scale is None else scale, int(bool(causal)), window, at + 3 * size,
              None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
              0 if ws is None else ws.numel())
     return y, lse
@@ -1007,6 +1034,8 @@ def moe_attention_decode(q: torch.Tensor, cache: KvCache, page_table: torch.Tens
         raise ValueError(f"moe_attention_decode: q is on GPU {gpu}, the cache on {cache.device}")
     qh = _heads("moe_attention_decode: q", q, (B, nq, cache.head_dim), gpu)
     y, lse, yh = _attention_out("moe_attention_decode", q, out, want_lse, gpu)
+    h = _packed(qh + yh, 2)
+    at = ctypes.addressof(h)
     if page_table.dtype is not torch.int32 or page_table.dim() != 2:
         raise ValueError(f"moe_attention_decode: page_table must be int32 [B][width], got {page_table.dtype}")
     width = page_table.shape[1]
@@ -1020,9 +1049,9 @@ def moe_attention_decode(q: torch.Tensor, cache: KvCache, page_table: torch.Tens
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
     else:
         _on_gpu("moe_attention_decode: workspace", ws, gpu)
-    _enqueue("moe_attention_decode", gpu, ctypes.addressof(qh), B, nq, cache.at, page_table.data_ptr(), stride, width,
+    _enqueue("moe_attention_decode", gpu, at, B, nq, cache.at, page_table.data_ptr(), stride, width,
              _ints("moe_attention_decode: lens", lens, (B,), gpu), max_len, D ** -0.5 if scale is None else scale, window,
-             ctypes.addressof(yh), None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
+             at + _HEADS_BYTES, None if lse is None else lse.data_ptr(), None if ws is None else ws.data_ptr(),
              0 if ws is None else ws.numel())
     return y, lse
 

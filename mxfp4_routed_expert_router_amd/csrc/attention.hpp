@@ -70,16 +70,16 @@ __device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballo
 // Partial results in a workspace: (m, l) of every row and part, then O.
 struct AttnParts {
   float* ml;  // [rows][parts][2]
-  float* o;   // [rows][parts][D]
+  float* o;   // [rows][parts][D], 16-byte aligned
   int parts;
 };
 inline size_t attn_parts_bytes(int64_t rows, int parts, int D) {
-  return parts > 1 ? (size_t)rows * parts * (size_t)(D + 2) * 4 : 0;
+  return parts > 1 ? (size_t)rows * parts * (size_t)(D + 2) * 4 + 8 : 0;
 }
 inline AttnParts attn_parts(void* ws, int64_t rows, int parts) {
   AttnParts p;
   p.ml = (float*)ws;
-  p.o = parts > 1 ? (float*)ws + 2 * rows * parts : nullptr;
+  p.o = parts > 1 ? (float*)ws + (2 * rows * parts + 3) / 4 * 4 : nullptr;
   p.parts = parts;
   return p;
 }
@@ -87,7 +87,7 @@ inline AttnParts attn_parts(void* ws, int64_t rows, int parts) {
 __device__ __forceinline__ AttnParts attn_parts_dev(void* ws, int64_t rows, int parts) {
   AttnParts p;
   p.ml = (float*)ws;
-  p.o = (float*)ws + 2 * rows * parts;
+  p.o = (float*)ws + (2 * rows * parts + 3) / 4 * 4;
   p.parts = parts;
   return p;
 }

@@ -29,6 +29,26 @@ __device__ __forceinline__ float other_half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// Sixteen bytes a lane from base + off straight into LDS, consecutive lanes behind one another from `to` on.  The compiler
+// waits for such loads of its own at the next LDS read that it cannot tell apart, in the middle of the tile that they
+// should overlap; written out (FREE), only loads_done() waits for them, which stands in front of the barrier that publishes
+// them either way.  Heads of 128: 4130 -> 4010 us for 16384 tokens.  With one wave on a SIMD (heads beyond 128) the
+// compiler's own order of loads and arithmetic is worth more: 342 us for 4096 tokens of heads of 256, so 395.
+// (The load has no registers to write; one instruction lies between a write of m0 and its use; nothing else in these
+// kernels uses m0.)
+template <bool FREE>
+__device__ __forceinline__ void load_to_lds(const void* base, uint32_t off, u32x4* to) {
+  if constexpr (FREE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds_address(to))), "v"(off), "s"(base)
+                 : "memory");
+  else
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const char*)base + off),
+                                     (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // Next in a block's order: READS LDS reads; a matrix product with TRANS exponentials, VALU vector instructions and READS
 // LDS reads behind it.
 template <int READS>
@@ -159,9 +179,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     v_off[u] = place(u, a.v_ts, true, BN);
   }
   const auto put = [&](const uint16_t* base, uint32_t off, u32x4* to) {
-    if (EXACT || off != ~0u)
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const char*)base + off),
-                                       (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+    if (EXACT || off != ~0u) load_to_lds<DP <= 128>(base, off, to);
   };
   const auto load_tile = [&](int buf, int v, const uint16_t* rows, int64_t ts, const uint32_t* off, int j0) {
     const uint16_t* from = rows + j0 * ts;
@@ -218,6 +236,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     const int j0 = b_lo + t * BN;
     const uint32_t buf = (t & 1) * 2 * kTile, buf_after = buf ^ (2 * kTile);
     // V of tile t is there, K too (kAhead: of tile t + 1), and nobody reads what the next loads replace any more
+    loads_done();
     __syncthreads();
     if (t + 1 + kAhead < n_tiles) load_k(t + 1 + kAhead);
     if (t + 1 < n_tiles) load_v(t + 1);
@@ -365,6 +384,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     f32x16 s0[KT], s1[KT];
     if constexpr (kAhead) {
       if (n_tiles > 1) load_k(1);
+      loads_done();
       __syncthreads();
       scores(s0, 0);
       // (behind the last tile the other buffer's scores are computed once more and not used)
