@@ -433,13 +433,13 @@ struct DecodePlan {
 };
 // Parts of a row of up to n keys (in a window: of what it can touch).  Few rows: 512 workgroups, of one step of their waves
 // at least (one sequence of 777 tokens: 8.7 us; two steps 9.6).  Up to 1024 units of row and head: 3072 workgroups of two
-// steps at least, which evens out rows of different lengths (us for 64 sequences of up to 8192: 1024 workgroups 245, 2048
+// steps at least, up to 64 to a row (three rows of 131072 in MXFP8 join in 9.3 us from 128 parts, in 5 from 43), which evens out rows of different lengths (us for 64 sequences of up to 8192: 1024 workgroups 245, 2048
 // 243, 3072 220, 6144 220; 16 of up to 16384 in MXFP8 82, 74, 74, 78; 8 of 4096 in steps of 128 29.6, of 256 27.7).  More
 // units are even enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long.
 int64_t most_parts(int64_t units, int64_t n) {
   constexpr int kBlockKeys = kDecodeWaves * kWaveKeys;
   const int64_t some = std::min((512 + units - 1) / units, (n + kBlockKeys - 1) / kBlockKeys);
-  const int64_t more = units < 1024 ? std::min((3072 + units - 1) / units, n / (2 * kBlockKeys))
+  const int64_t more = units < 1024 ? std::min(std::min<int64_t>((3072 + units - 1) / units, 64), n / (2 * kBlockKeys))
                                     : std::min<int64_t>(16, n / 8192);
   return std::max<int64_t>(1, std::max(some, more));
 }
@@ -462,7 +462,7 @@ void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
   if (a.D <= 64) MOE_DECODE(64, 4);
   else if (a.D <= 96) MOE_DECODE(96, 2);
   else if (a.D <= 128) MOE_DECODE(128, 2);
-  else if (a.D <= 192) MOE_DECODE(192, 2);
+  else if (a.D <= 192) MOE_DECODE(192, (FMT == MOE_KV_MXFP8 ? 2 : 1));  // (16 bits, 64 rows of up to 4096: 176 us, so 227)
   else MOE_DECODE(256, 1);
 #undef MOE_DECODE
 #undef MOE_DECODE_W

@@ -184,6 +184,18 @@ def test_prompt_edges_of_the_mask():
     ref.check(lse[:n, 0], torch.log(i - first + 1), torch.full((n,), 1e-6, dtype=torch.float64), "count")
 
 
+@pytest.mark.parametrize("D,window", [(64, 0), (128, 100), (256, 40)])
+def test_prompt_waves_without_a_share(D, window):
+    """One query head per key-value head: a workgroup's waves stand at different tokens, so some have no part in a tile
+    that they load for the others.  The same bits every time, and the right ones."""
+    q, k, v, cu_q, cu_k = prompt_inputs([700, 129], [700, 129], 8, 8, D, "bf16", 6)
+    first, _ = run_prompt(q, k, v, cu_q, cu_k, True, window, what=f"waves D={D} window={window}")
+    c = torch.tensor(cu_q, dtype=torch.int32, device=DEV)
+    for _ in range(20):
+        y, _ = moe.moe_attention_prompt(q, k, v, c, window=window)
+        assert torch.equal(y[:cu_q[-1]], first[:cu_q[-1]])
+
+
 def test_prompt_same_bits_again_and_on_other_streams():
     q, k, v, cu_q, cu_k = prompt_inputs([1000, 77], [1000, 400], 8, 2, 128, "bf16", 4)
     cq, ck = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (cu_q, cu_k))
