@@ -1,6 +1,8 @@
 /*
  * moe.h -- C ABI of the routed Mixture-of-Experts feed-forward layer for AMD Instinct MI355X
- * (gfx950).  Four calls make one layer: moe_route -> moe_bucket -> moe_expert_ffn -> moe_combine.
+ * (gfx950).  Four calls make one layer: moe_route -> moe_bucket -> moe_expert_ffn -> moe_combine.  In front of it
+ * stand moe_linear, moe_add_rms_norm and moe_route_grouped, and the attention: moe_rope_cache -> moe_attention_prompt or
+ * moe_attention_decode.
  *
  * Sources (cited by page title and section; the pages print no code):
  *  [NV]  same post and section: NVFP4 also stores E2M1 values, with an E4M3 scale per 16 values
@@ -34,8 +36,8 @@
  *  - Validation happens before anything is enqueued; on any error nothing is launched and the
  *    status says why.  T == 0 returns MOE_OK without touching any pointer.
  *  - Inputs are read-only; outputs are overwritten (never accumulated into); buffers must not
- *    alias each other (but moe_add_rms_norm's residual_out may be its residual).  Calls that share
- *    no output buffer and no workspace may run concurrently on different streams.
+ *    alias each other (but moe_add_rms_norm's residual_out may be its residual, moe_rope_cache's outputs its
+ *    inputs).  Calls that share no output buffer and no workspace may run concurrently on different streams.
  *  - Results are deterministic: the same inputs give bit-identical outputs on every run (no
  *    floating-point atomics anywhere).
  */
@@ -64,7 +66,7 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_ACT_BF16 = 0, MOE_ACT_FP16 = 1 } moe_act_dtype;
-/* Storage types of moe_add_rms_norm, moe_select_experts and moe_linear (the first two as above). */
+/* Storage types of moe_add_rms_norm, moe_select_experts, moe_linear and the attention (the first two as above). */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_FP16 = 1, MOE_DT_FP32 = 2 } moe_dtype;
 typedef enum { MOE_W_MXFP4 = 0, MOE_W_FP16 = 1, MOE_W_INT4_G32 = 2, MOE_W_NVFP4 = 3 } moe_w_format;
 

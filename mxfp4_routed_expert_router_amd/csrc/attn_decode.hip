@@ -7,7 +7,8 @@
 // kernel, so the second product costs nothing and only the output is rounded.
 //
 // Consecutive lanes read consecutive 16 bytes of a token's row, whole 128-byte lines a load and past the caches: in MFMA
-// layout at once (64 bytes of sixteen rows a load) 176 sequences of up to 4096 tokens take 266 us, so 222.  The tile then
+// layout at once (64 bytes of sixteen rows a load) 176 sequences of up to 4096 tokens take 266 us, so 215 (5.6 TB/s; reading
+// alone reaches 7.17).  The tile then
 // turns through a part of LDS that is the wave's own.  The next tile's K and V are on their way meanwhile.
 //
 // 16-bit caches are operands as they are, E4M3 codes times a power of two are exact in bf16.
@@ -431,16 +432,18 @@ __global__ __launch_bounds__(256) void attn_join_few_kernel(AttnJoin a) {
 struct DecodePlan {
   int parts, part_keys;
 };
-// Parts of a row of up to n keys (in a window: of what it can touch).  Few rows: 512 workgroups, of one step of their waves
-// at least (one sequence of 777 tokens: 8.7 us; two steps 9.6).  Up to 1024 units of row and head: 3072 workgroups of two
-// steps at least, up to 64 to a row (three rows of 131072 in MXFP8 join in 9.3 us from 128 parts, in 5 from 43), which evens out rows of different lengths (us for 64 sequences of up to 8192: 1024 workgroups 245, 2048
-// 243, 3072 220, 6144 220; 16 of up to 16384 in MXFP8 82, 74, 74, 78; 8 of 4096 in steps of 128 29.6, of 256 27.7).  More
-// units are even enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long.
+// Parts of a row of up to n keys (in a window: of what it can touch).  Few rows: two workgroups a CU, of one step of their
+// waves at least (one sequence of 777 tokens: 8.7 us; two steps 9.6).  Up to four units of row and head a CU: twelve
+// workgroups a CU, of two steps at least, up to 64 to a row (three rows of 131072 in MXFP8 join in 9.3 us from 128 parts, in
+// 5 from 43), which evens out rows of different lengths (us with 4, 8, 12, 24 a CU: 64 sequences of up to 8192 245, 243,
+// 220, 220; 16 of up to 16384 in MXFP8 82, 74, 74, 78; 8 of 4096 in steps of 128 29.6, of 256 27.7).  More units are even
+// enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long.
 int64_t most_parts(int64_t units, int64_t n) {
-  constexpr int kBlockKeys = kDecodeWaves * kWaveKeys;
-  const int64_t some = std::min((512 + units - 1) / units, (n + kBlockKeys - 1) / kBlockKeys);
-  const int64_t more = units < 1024 ? std::min(std::min<int64_t>((3072 + units - 1) / units, 64), n / (2 * kBlockKeys))
-                                    : std::min<int64_t>(16, n / 8192);
+  constexpr int kBlockKeys = kDecodeWaves * kWaveKeys, kCus = 256;
+  const auto for_blocks = [&](int64_t blocks) { return (blocks + units - 1) / units; };
+  const int64_t some = std::min(for_blocks(2 * kCus), (n + kBlockKeys - 1) / kBlockKeys);
+  const int64_t more = units < 4 * kCus ? std::min(std::min<int64_t>(for_blocks(12 * kCus), 64), n / (2 * kBlockKeys))
+                                        : std::min<int64_t>(16, n / 8192);
   return std::max<int64_t>(1, std::max(some, more));
 }
 int64_t decode_units(int B, int Hq, int Hkv) { return (int64_t)B * Hkv * ((Hq / Hkv + 15) / 16); }
