@@ -1213,8 +1213,8 @@ class AttentionBlock:
         if residual_out is None:
             residual_out = torch.empty_like(residual)
         moe_add_rms_norm(x, self.norm, residual, out=(self.x[:t], residual_out, None, None))
-        qkv = moe_linear(self.x[:t], self.W_qkv, out=self.qkv[:t]).view(t, -1, self.cache.head_dim)
         n, m = self.n_q_heads, self.cache.n_kv_heads
+        qkv = moe_linear(self.x[:t], self.W_qkv, out=self.qkv[:t]).view(t, n + 2 * m, self.cache.head_dim)
         moe_rope_cache(qkv[:, :n], qkv[:, n:n + m], qkv[:, n + m:], self.rope,
                        None if self.rope is None else positions, self.cache, slots,
                        out=(self.q[:t], self.k[:t] if packed else None, self.v[:t] if packed else None))
@@ -1224,7 +1224,7 @@ class AttentionBlock:
                cu: torch.Tensor, residual_out: Optional[torch.Tensor] = None):
         t, residual_out = self._front(x, residual, positions, slots, residual_out, True)
         moe_attention_prompt(self.q[:t], self.k[:t], self.v[:t], cu, window=self.window, out=(self.y[:t], None))
-        return self.y[:t].view(t, -1), residual_out
+        return self.y[:t].flatten(1), residual_out
 
     def decode(self, x: torch.Tensor, residual: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
                page_table: torch.Tensor, lens: torch.Tensor, max_len: Optional[int] = None,
@@ -1232,7 +1232,7 @@ class AttentionBlock:
         t, residual_out = self._front(x, residual, positions, slots, residual_out, False)
         moe_attention_decode(self.q[:t], self.cache, page_table, lens, max_len, window=self.window,
                              out=(self.y[:t], None))
-        return self.y[:t].view(t, -1), residual_out
+        return self.y[:t].flatten(1), residual_out
 
 
 class FixedShapeLayer:

@@ -437,13 +437,14 @@ struct DecodePlan {
 // workgroups a CU, of two steps at least, up to 64 to a row (three rows of 131072 in MXFP8 join in 9.3 us from 128 parts, in
 // 5 from 43), which evens out rows of different lengths (us with 4, 8, 12, 24 a CU: 64 sequences of up to 8192 245, 243,
 // 220, 220; 16 of up to 16384 in MXFP8 82, 74, 74, 78; 8 of 4096 in steps of 128 29.6, of 256 27.7).  More units are even
-// enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long.
+// enough (176 sequences of up to 4096: one part 215, two 227, three 221) unless rows are very long; past 64 units a CU
+// parts would only take workspace.
 int64_t most_parts(int64_t units, int64_t n) {
   constexpr int kBlockKeys = kDecodeWaves * kWaveKeys, kCus = 256;
   const auto for_blocks = [&](int64_t blocks) { return (blocks + units - 1) / units; };
   const int64_t some = std::min(for_blocks(2 * kCus), (n + kBlockKeys - 1) / kBlockKeys);
   const int64_t more = units < 4 * kCus ? std::min(std::min<int64_t>(for_blocks(12 * kCus), 64), n / (2 * kBlockKeys))
-                                        : std::min<int64_t>(16, n / 8192);
+                                        : (units < 64 * kCus ? std::min<int64_t>(16, n / 8192) : 1);
   return std::max<int64_t>(1, std::max(some, more));
 }
 int64_t decode_units(int B, int Hq, int Hkv) { return (int64_t)B * Hkv * ((Hq / Hkv + 15) / 16); }

@@ -92,6 +92,31 @@ def test_prompt_ragged(nq, nk, causal):
     prompt(nq, nk, 4, 2, 64, causal=causal, seed=len(nq))
 
 
+@pytest.mark.parametrize("n", [63, 64, 65, 129, 400, 5000])
+def test_prompt_many_sequences(n):
+    """Sequences of 0 to 4 tokens, some with more keys: their places are searched for, 64 at a step."""
+    nq = [(7 * i) % 5 for i in range(n)]
+    prompt(nq, [x + (i % 3) for i, x in enumerate(nq)], 3, 1, 16, seed=n)
+    if n == 400:
+        nq[200], nq[399] = 300, 150
+        prompt(nq, nq, 5, 1, 64, seed=n)
+
+
+@pytest.mark.parametrize("cu", [[0, 300, 100, 40, 400, 200, 350], [-7, 50, 20, 2 ** 31 - 1, 10, 300, 400], [400, 0, 400], [400, 100]])
+@pytest.mark.parametrize("Tk", [400, 9000])
+def test_prompt_sequences_out_of_order(cu, Tk):
+    """Offsets that descend or leave the rows have no defined result, but nothing outside q's rows is written."""
+    n, guard = 400, 64
+    q, k, v, _, _ = prompt_inputs([n], [Tk], 4, 2, 64, "bf16", 5, tail=0)
+    y = torch.full((n + 2 * guard, 4, 64), 7.0, dtype=q.dtype, device=DEV)
+    lse = torch.full((n + 2 * guard, 4), 7.0, device=DEV)
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    moe.moe_attention_prompt(q, k, v, c, out=(y[guard:-guard], lse[guard:-guard]))
+    torch.cuda.synchronize()
+    for t in (y, lse):
+        assert bool((t[:guard] == 7.0).all()) and bool((t[-guard:] == 7.0).all())
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 1000])
 @pytest.mark.parametrize("G", [1, 4])
 def test_prompt_windows(window, G):

@@ -187,6 +187,16 @@ def test_decoder_block(mx):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+def test_no_tokens():
+    block = make(4)[0]
+    x, res = inputs(0)
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    attn, r = block.prompt(x, res, none, none, ints([0, 0]))
+    assert attn.shape == (0, HQ * D) and r.shape == (0, H)
+    attn, r = block.decode(x, res, none, none, torch.zeros(0, 3, dtype=torch.int32, device=DEV), none)
+    assert attn.shape == (0, HQ * D)
+
+
 def test_refusals():
     block = make(4)[0]
     x, res = inputs(5)
