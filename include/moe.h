@@ -567,7 +567,7 @@ moe_status moe_rope_cache(const moe_rope *rope, const int32_t *positions, int T,
  *         multiples of 8 values
  *   lse   [Tq][n_q_heads] fp32, or NULL
  *   workspace moe_attention_prompt_workspace_bytes(...) bytes, 16-byte aligned (NULL if that is 0)
- * Errors: NULL, SHAPE (Tq<0, Tk<0, n_seqs<0 or >2^20, heads, head_dim, Tq * n_q_heads or Tq + Tk from 2^31 on, more than
+ * Errors: NULL, SHAPE (Tq<0, Tk<0, n_seqs<0 or >2^20, heads, head_dim, Tq * n_q_heads from 2^31 on, Tq + Tk > 2^30, more than
  * 2^23 workgroups, a scale that is not positive and finite, window<0 or without causal), DTYPE, ALIGN, WORKSPACE, HIP. */
 size_t moe_attention_prompt_workspace_bytes(int Tq, int Tk, int n_seqs, int n_q_heads, int n_kv_heads, int head_dim);
 moe_status moe_attention_prompt(const moe_heads *q, const moe_heads *k, const moe_heads *v, const int32_t *cu_q,

@@ -3,6 +3,7 @@
 #include <limits.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -972,8 +973,8 @@ moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const mo
     if ((st = check_heads(*h, 8)) != MOE_OK) return st;
   }
   if (!usable_scale(scale) || window < 0 || (window > 0 && !causal)) return MOE_ERR_SHAPE;
-  // rows of a key-value head, and keys one behind another's last query, are 31-bit numbers
-  if ((int64_t)Tq * n_q_heads > INT_MAX || (int64_t)Tq + Tk > INT_MAX || n_seqs > 1 << 20) return MOE_ERR_SHAPE;
+  // rows of a key-value head, positions, and the first key behind a row's last share are 31-bit numbers
+  if ((int64_t)Tq * n_q_heads > INT_MAX || (int64_t)Tq + Tk > 1 << 30 || n_seqs > 1 << 20) return MOE_ERR_SHAPE;
   // (64 keys of a tile are addressed with 32-bit offsets)
   if (k->token_stride >= 1 << 24 || v->token_stride >= 1 << 24) return MOE_ERR_SHAPE;
   if (!al4(cu_q) || !al4(cu_k) || (lse && !al4(lse))) return MOE_ERR_ALIGN;
@@ -1007,7 +1008,7 @@ moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const mo
   a.G = moe::fast_div((uint32_t)(n_q_heads / n_kv_heads));
   a.c = base2_scale(scale);
   a.causal = causal != 0;
-  a.window = window;
+  a.window = std::min(window, std::max(Tk, 1));  // (past Tk it hides nothing; positions minus it stay 32-bit numbers)
   a.ws = workspace;
   return hip_status(moe::launch_prompt(a, (hipStream_t)stream));
 }

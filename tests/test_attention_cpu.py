@@ -89,7 +89,7 @@ def test_prompt_refusals():
                 dict(nq=1026, nkv=2), dict(D=4), dict(D=65), dict(D=264), dict(scale=0.0), dict(scale=-1.0),
                 dict(scale=math.nan), dict(scale=math.inf), dict(scale=3e38), dict(window=-1), dict(window=5, causal=0),
                 dict(Tq=1 << 30), dict(Tq=1 << 24, Tk=(1 << 31) - 5, nq=4), dict(q=heads(ts=-8)), dict(v=heads(hs=1 << 41)),
-                dict(Tq=1 << 21, nq=256, nkv=1)):
+                dict(Tq=1 << 21, nq=256, nkv=1), dict(Tq=8, Tk=(1 << 30) - 7)):
         assert f(**bad) == SHAPE, bad
     for bad in (dict(q=heads(dt=FP32)), dict(k=heads(dt=FP16)), dict(y=heads(dt=FP16)), dict(v=heads(dt=7)),
                 dict(**{x: heads(dt=FP32) for x in "qkvy"})):

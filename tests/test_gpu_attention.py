@@ -123,6 +123,13 @@ def test_prompt_windows(window, G):
     prompt([330, 50], [330, 90], 4, 4 // G, 64, "fp16", window=window, seed=window)
 
 
+@pytest.mark.parametrize("window", [200, 2 ** 30, 2 ** 31 - 1])
+def test_prompt_windows_past_the_keys(window):
+    """Also for queries in front of the first key, whose positions are negative."""
+    prompt([10, 150, 64], [5, 20, 200], 4, 2, 64, window=window, seed=8)
+    prompt([3], [5000], 4, 2, 64, window=window + (0 if window > 200 else 4800), seed=8)
+
+
 @pytest.mark.parametrize("layout", ["tokens", "heads"])
 @pytest.mark.parametrize("D", [64, 96, 128])
 def test_prompt_strides(layout, D):
@@ -333,6 +340,11 @@ def test_decode_long(n, fmt, B):
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
 def test_decode_windows(window, fmt):
     decode([3, 64, 65, 1000, 2500], 48, 4, 2, 64, fmt, window=window, seed=window)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_decode_windows_past_the_keys(fmt):
+    decode([1, 0, 700, 64], 16, 8, 2, 64, fmt, window=2 ** 31 - 1)
 
 
 @pytest.mark.parametrize("order", ["token", "head first", "padded"])
