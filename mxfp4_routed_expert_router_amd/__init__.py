@@ -1189,7 +1189,7 @@ class AttentionBlock:
     prompt(x, residual, positions, slots, cu) attends each sequence over its own rows, decode(x, residual, positions,
     slots, page_table, lens) each row over its cached tokens, its own (written to slots[b]) among them.  Both -> (attn
     [T'][n_q_heads * head_dim], residual_out), which MoEBlock.forward takes; x (an MoEBlock's y, or embeddings) and
-    residual are [T'][hidden] for T' <= T tokens."""
+    residual are [T'][hidden] for T' <= T tokens.  attn lies in the block's buffer: the next pass writes over it."""
 
     def __init__(self, W_qkv: LinearWeights, T: int, norm: RmsNorm, n_q_heads: int, cache: KvCache,
                  rope: Optional[Rope] = None, window: int = 0):

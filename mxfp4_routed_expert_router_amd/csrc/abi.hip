@@ -837,6 +837,11 @@ moe_status check_heads(const moe_heads& h, int unit) {
     return MOE_ERR_ALIGN;
   return MOE_OK;
 }
+// Rows that are written: of `n` along a stride, no two may be the same (broadcast) or half over each other.
+inline bool overlaps(int64_t n, int64_t stride, int64_t values) { return n > 1 && stride < values; }
+inline bool overlaps(const moe_heads& h, int T, int n_heads, int head_dim) {
+  return overlaps(T, h.token_stride, head_dim) || overlaps(n_heads, h.head_stride, head_dim);
+}
 moe_status check_cache(const moe_kv_cache& c) {
   if (c.fmt != MOE_KV_BF16 && c.fmt != MOE_KV_FP16 && c.fmt != MOE_KV_MXFP8) return MOE_ERR_DTYPE;
   const bool mx = c.fmt == MOE_KV_MXFP8;
@@ -903,6 +908,7 @@ moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T,
     if (!in[i]) continue;
     if (dt >= 0 && in[i]->dtype != dt) return MOE_ERR_DTYPE;
     dt = in[i]->dtype;
+    if (out[i] && overlaps(*out[i], T, i == 0 ? n_q_heads : n_kv_heads, head_dim)) return MOE_ERR_SHAPE;
     if (out[i] && out[i]->p == in[i]->p && (out[i]->dtype != dt || out[i]->token_stride != in[i]->token_stride ||
                                             out[i]->head_stride != in[i]->head_stride))
       return MOE_ERR_SHAPE;
@@ -926,6 +932,14 @@ moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T,
     const moe_status st = check_cache(*cache);
     if (st != MOE_OK) return st;
     if (cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim) return MOE_ERR_SHAPE;
+    const auto rows = [&](int64_t page, int64_t head, int64_t token, int64_t values) {
+      return overlaps(cache->n_pages, page, values) || overlaps(n_kv_heads, head, values) ||
+             overlaps(cache->page_size, token, values);
+    };
+    if (rows(cache->page_stride, cache->head_stride, cache->token_stride, head_dim) ||
+        (cache->fmt == MOE_KV_MXFP8 &&
+         rows(cache->s_page_stride, cache->s_head_stride, cache->s_token_stride, head_dim / 32)))
+      return MOE_ERR_SHAPE;
     if (!al4(slots)) return MOE_ERR_ALIGN;
     a.fmt = cache->fmt;
     a.n_slots = cache->n_pages * cache->page_size;
@@ -973,6 +987,7 @@ moe_status moe_attention_prompt(const moe_heads* q, const moe_heads* k, const mo
     if ((st = check_heads(*h, 8)) != MOE_OK) return st;
   }
   if (!usable_scale(scale) || window < 0 || (window > 0 && !causal)) return MOE_ERR_SHAPE;
+  if (overlaps(*y, Tq, n_q_heads, head_dim)) return MOE_ERR_SHAPE;
   // rows of a key-value head, positions, and the first key behind a row's last share are 31-bit numbers
   if ((int64_t)Tq * n_q_heads > INT_MAX || (int64_t)Tq + Tk > 1 << 30 || n_seqs > 1 << 20) return MOE_ERR_SHAPE;
   // (64 keys of a tile are addressed with 32-bit offsets)
@@ -1035,7 +1050,7 @@ moe_status moe_attention_decode(const moe_heads* q, int B, int n_q_heads, const 
   if (!usable_scale(scale) || window < 0 || max_len < 0 || max_len > 1 << 30 || table_width < 0 ||
       max_len > (int64_t)table_width * cache->page_size || table_stride < 0 || table_stride > kMostStride)
     return MOE_ERR_SHAPE;
-  if ((int64_t)B * n_q_heads > kMostBlocks) return MOE_ERR_SHAPE;
+  if ((int64_t)B * n_q_heads > kMostBlocks || overlaps(*y, B, n_q_heads, cache->head_dim)) return MOE_ERR_SHAPE;
   if (!al4(page_table) || !al4(lens) || (lse && !al4(lse))) return MOE_ERR_ALIGN;
   const size_t need =
       moe_attention_decode_workspace_bytes(B, n_q_heads, cache->n_kv_heads, cache->head_dim, max_len);

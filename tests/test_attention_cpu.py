@@ -141,6 +141,27 @@ def test_decode_refusals(fmt):
         assert L.moe_attention_decode_workspace_bytes(*bad) == 0
 
 
+def test_outputs_that_overlap():
+    """Rows of one output over each other (a broadcast one) would be written by several workgroups at once."""
+    L = m.lib()
+    out = P + 0x10000
+    for ts, hs in ((0, 64), (256, 0), (32, 128), (256, 56)):
+        y = heads(out, ts=ts, hs=hs)
+        assert L.moe_attention_prompt(ref_(heads()), ref_(heads()), ref_(heads()), P, P, 2, 8, 8, 4, 2, 64, 0.125, 1, 0,
+                                      ref_(y), None, None, 0, None) == SHAPE
+        assert L.moe_attention_decode(ref_(heads()), 3, 4, ref_(cache_desc(m.MOE_KV_BF16)), P, 10, 10, P, 16, 0.125, 0,
+                                      ref_(y), None, None, 0, None) == SHAPE
+        for at in range(3):
+            outs = [ref_(y if i == at else heads(out + 4096 * i)) for i in range(3)]
+            assert L.moe_rope_cache(None, None, 4, 4, 2, 64, ref_(heads()), ref_(heads()), ref_(heads()), *outs, None, None,
+                                    None) == SHAPE
+    for fmt in (m.MOE_KV_BF16, m.MOE_KV_FP16, m.MOE_KV_MXFP8):
+        names = ["page_stride", "head_stride", "token_stride"]
+        for name in names + ["s_" + n for n in names] * (fmt == m.MOE_KV_MXFP8):
+            assert L.moe_rope_cache(None, None, 4, 0, 2, 64, None, ref_(heads()), ref_(heads()), None, None, None,
+                                    ref_(cache_desc(fmt, **{name: 0})), P, None) == SHAPE
+
+
 def test_workspaces_stay_small():
     """The parts of a row are few where rows are many: a workspace never passes the 16-bit rows it serves by far."""
     L = m.lib()
