@@ -9,7 +9,8 @@
 // Consecutive lanes read consecutive 16 bytes of a token's row, whole 128-byte lines a load and past the caches: in MFMA
 // layout at once (64 bytes of sixteen rows a load) 176 sequences of up to 4096 tokens take 266 us, so 215 (5.6 TB/s; reading
 // alone reaches 7.17).  The tile then
-// turns through a part of LDS that is the wave's own.  The next tile's K and V are on their way meanwhile.
+// turns through a part of LDS that is the wave's own.  The next tile's K and V are on their way meanwhile (MXFP8 from heads of
+// 128 on: one of them).
 //
 // 16-bit caches are operands as they are, E4M3 codes times a power of two are exact in bf16.
 #include <algorithm>
@@ -50,8 +51,14 @@ template <int FMT, int DP, bool EXACT, bool WHOLE, int PER_SIMD>
 __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(DecodeArgs a) {
   constexpr bool F16 = FMT == MOE_KV_FP16, MX = FMT == MOE_KV_MXFP8;
   constexpr int ST = DP / 32, CT = DP / 16, W = kDecodeWaves;
+  // V of a tile is asked for when its K is in LDS, and the next K when V is, so that one of them is in registers at a time.
+  // In MXFP8 that is what lets two waves of heads of 256 share a SIMD (64 rows of up to 4096: 229 -> 132 us; of 160 148 ->
+  // 140, of 128 the same within 1%); 16-bit rows lose by it (heads of 128: 215 -> 217).
+  constexpr bool kLate = MX && DP >= 128;
+  // Rows of a power of two: a lane's LDS addresses differ by exclusive-ors with constants and by constants.
+  constexpr bool kXor = (DP & (DP - 1)) == 0;
   typedef Rows<FMT, DP> R;
-  __shared__ __attribute__((aligned(256))) u32x4 tiles[W][kWaveKeys * DP / 8];  // K, then V, of 16 bits; in the end O
+  __shared__ __attribute__((aligned(512))) u32x4 tiles[W][kWaveKeys * DP / 8];  // K, then V, of 16 bits; in the end O
   __shared__ float stat[W][2][16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, g = lane >> 4;
@@ -157,6 +164,14 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   };
   // A tile into LDS as 16-bit rows; rows of masked keys as zeros where those are asked for (0 * NaN is no zero).
   const uint32_t lds0 = lds_address(tiles[wave]);
+  uint32_t put_k = 0, put_v = 0, get_k = 0, get_v = 0;
+  if constexpr (kXor) {
+    const int row = lane / R::CH, ch = lane % R::CH * (MX ? 2 : 1), v_row = 4 * g + (r >> 2);
+    put_k = lds0 + row * (2 * DP) + ((ch ^ swizzle_k<DP>(row)) << 4);
+    put_v = lds0 + row * (2 * DP) + ((ch ^ swizzle_v<DP>(row)) << 4);
+    get_k = lds0 + r * (2 * DP) + ((g ^ swizzle_k<DP>(r)) << 4);
+    get_v = lds0 + v_row * (2 * DP) + ((((r & 3) >> 1) ^ swizzle_v<DP>(v_row)) << 4) + ((r & 1) << 3);
+  }
   const auto store = [&](const R& t, bool v, uint32_t keep) {
 #pragma unroll
     for (int n = 0; n < R::N; ++n) {
@@ -167,7 +182,16 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = (keep >> row) & 1 ? x[i] : 0u;
       }
-      u32x4* to_row = &tiles[wave][row * (DP / 8)];
+      const auto to = [&](int ch, u32x4 w) {  // (ch: the lane's 16-bit chunk, or the one behind it)
+        if constexpr (kXor) {
+          const int first = n * (64 / R::CH);
+          const int turn = (v ? swizzle_v<DP>(first) : swizzle_k<DP>(first)) ^ (MX ? ch & 1 : 0);
+          const uint32_t at = (v ? put_v : put_k) ^ (turn << 4);
+          *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(at + first * (2 * DP)) = w;
+        } else {
+          tiles[wave][row * (DP / 8) + (ch ^ sw)] = w;
+        }
+      };
       if constexpr (MX) {
         uint32_t code = 0;
 #pragma unroll
@@ -182,10 +206,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
           y[i >> 1][2 * (i & 1)] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], s, false));
           y[i >> 1][2 * (i & 1) + 1] = bitcast<uint32_t>(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[i], s, true));
         }
-        to_row[(2 * c) ^ sw] = y[0];
-        to_row[(2 * c + 1) ^ sw] = y[1];
+        to(2 * c, y[0]);
+        to(2 * c + 1, y[1]);
       } else {
-        to_row[c ^ sw] = x;
+        to(c, x);
       }
     }
   };
@@ -203,18 +227,25 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     look_up(start + kStep);
     load_scales();
     load(k, a.cache_k);
-    load(v, a.cache_v);
+    if constexpr (!kLate) load(v, a.cache_v);
   }
   for (int j0 = start; j0 < to; j0 += kStep) {
     const uint32_t now = seen;
     const bool more = j0 + kStep < to;
+    // (the addresses are made anew in each tile: kept, they would cost the registers that the second wave needs)
+    if constexpr (kLate && kXor) asm volatile("" : "+v"(put_k), "+v"(put_v), "+v"(get_k), "+v"(get_v));
     store(k, false, now);
-    if constexpr (MX) sc_now = sc;
-    if (more) {
+    const auto next = [&]() {
       place(j0 + kStep);
       look_up(j0 + 2 * kStep);
       load_scales();
       load(k, a.cache_k);
+    };
+    if constexpr (kLate) {
+      load(v, a.cache_v);
+    } else {
+      if constexpr (MX) sc_now = sc;
+      if (more) next();
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -223,8 +254,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     for (int st = 0; st < ST; ++st)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        s[h] = mfma_16x16x32<F16>(lds_16(lds0 + (16 * h + r) * (2 * DP) + (((4 * st + g) ^ swizzle_k<DP>(16 * h + r)) << 4)),
-                                  qf[st], s[h]);
+        s[h] = mfma_16x16x32<F16>(
+            lds_16(kXor ? (get_k ^ (st << 6)) + 16 * h * (2 * DP)
+                        : lds0 + (16 * h + r) * (2 * DP) + (((4 * st + g) ^ swizzle_k<DP>(16 * h + r)) << 4)),
+            qf[st], s[h]);
     // m: reference of the exponents (base 2, scaled).  It rises only when some head's maximum passes it by more than 2^8.
     const float base = m == -INFINITY ? 0.0f : m;
     float top = -INFINITY;
@@ -264,7 +297,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
       }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    if constexpr (MX) {  // (the next tile's scales are on their way already)
+    if constexpr (MX && !kLate) {  // (the next tile's scales are on their way already)
       const RowScales<DP> next_sc = sc;
       sc = sc_now;
       store(v, true, now);
@@ -272,7 +305,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
     } else {
       store(v, true, now);
     }
-    if (more) load(v, a.cache_v);
+    if (more) {
+      if constexpr (kLate) next();
+      else load(v, a.cache_v);
+    }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
@@ -281,7 +317,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int row = 16 * h + 4 * g + (r >> 2), d = 16 * i + 4 * (r & 3);
-        const u32x2 t = lds_tr(lds0 + row * (2 * DP) + (((d >> 3) ^ swizzle_v<DP>(row)) << 4) + ((d & 7) << 1));
+        const u32x2 t = lds_tr(kXor ? (get_v ^ (i << 5)) + 16 * h * (2 * DP)
+                                    : lds0 + row * (2 * DP) + (((d >> 3) ^ swizzle_v<DP>(row)) << 4) + ((d & 7) << 1));
         w[2 * h] = t[0];
         w[2 * h + 1] = t[1];
       }
@@ -467,7 +504,7 @@ void launch_decode_fmt(const DecodeArgs& a, dim3 g, hipStream_t stream) {
   else if (a.D <= 96) MOE_DECODE(96, 2);
   else if (a.D <= 128) MOE_DECODE(128, 2);
   else if (a.D <= 192) MOE_DECODE(192, (FMT == MOE_KV_MXFP8 ? 2 : 1));  // (16 bits, 64 rows of up to 4096: 176 us, so 227)
-  else MOE_DECODE(256, 1);
+  else MOE_DECODE(256, (FMT == MOE_KV_MXFP8 ? 2 : 1));  // (16 bits, 64 rows of up to 4096: 212-230 us, so 270)
 #undef MOE_DECODE
 #undef MOE_DECODE_W
 }
