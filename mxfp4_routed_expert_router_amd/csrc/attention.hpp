@@ -1,9 +1,9 @@
 // What the prompt and the decode attention share: 16-bit MFMA operands, base-2 exponentials, and the partial results of
 // key ranges that several workgroups share.
 //
-// A row (one query head of one token) over keys j: s_j = c q.k_j with c = scale * log2(e), m >= max s_j - 8,
-// l = sum 2^(s_j - m), O = sum 2^(s_j - m) v_j; then y = O / l and lse = (m + log2 l) ln 2.  Parts of a row's keys join
-// by M = max m, l = sum l_p 2^(m_p - M), O likewise.
+// A row (one query head of one token) over keys j: s_j = c q.k_j with c = scale * log2(e), l = sum 2^(s_j - m),
+// O = sum 2^(s_j - m) v_j for a reference m (struct Reference); then y = O / l and lse = (m + log2 l) ln 2.  Parts of a
+// row's keys join by M = max m, l = sum l_p 2^(m_p - M), O likewise.
 #pragma once
 #include "launch.hpp"
 #include "values.hpp"
@@ -66,6 +66,40 @@ __device__ __forceinline__ int swizzle_v(int row) {
 
 // (a ballot is uniform to the compiler, __any() is not: its branches would keep both sides' values in registers)
 __device__ __forceinline__ bool wave_any(bool v) { return __builtin_amdgcn_ballot_w64(v) != 0; }
+
+// The reference m of a row's exponentials 2^(s - m), which are rounded to 16 bits, while l and O stay fp32.
+//   bf16 has fp32's exponents: m is the first tile's maximum and rises only when a later one passes it by more than 2^8, so
+// that factors are rare.
+//   fp16 ends at 2^-24, and with m at the maximum a weight 2^-20 of it kept four bits, one of 2^-25 none: a row whose largest
+// weight meets a value near zero came out percents off.  So m follows the tiles both ways: a tile's largest exponential
+// stands between 2^0 and 2^15.5 (65504 is the type's end), and a move, by a power of two that O and l take exactly, puts it
+// at 2^7.5, half way.  Then a weight of 2^-14 of its tile's largest or more has all its bits, and a smaller one is off by
+// 2^-25 of that largest at most; in the tile of the row's largest, which never stands below 2^7, it is 2^-21 and 2^-32.  m
+// falls no further than 40 below where it last rose, so that O stays inside fp32.  Each row moves by itself, whatever
+// its neighbours in the wave hold.  8192 tokens, 32 heads of 128 on 8: 551 us, with m at the maximum 545; a narrower range
+// (2^6 to 2^15.5, moved to 2^11) costs a move in many tiles: 587.
+template <bool F16>
+struct Reference {
+  static constexpr float kMost = F16 ? 15.5f : 8.0f, kLeast = 0.0f, kAt = F16 ? 7.5f : 0.0f, kFall = 40.0f;
+  float m = -INFINITY, floor = -INFINITY;
+  // top: the largest s - m of a tile (m still -inf: the largest s)
+  __device__ __forceinline__ bool moves(float top) const {
+    bool r = (top > kMost) | ((m == -INFINITY) & (top > -INFINITY));
+    if constexpr (F16) r |= (top < kLeast) & (top > -INFINITY);
+    return r;
+  }
+  // How far m goes up; before the first key O and l are zero.
+  __device__ __forceinline__ float way(float top) const {
+    if (m == -INFINITY) return top == -INFINITY ? 0.0f : top - kAt;
+    if constexpr (F16) return moves(top) ? fmaxf(__builtin_rintf(top - kAt), floor - m) : 0.0f;
+    else return fmaxf(top, 0.0f);
+  }
+  __device__ __forceinline__ float factor(float up) const { return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up); }
+  __device__ __forceinline__ void move(float top, float up) {
+    m = m == -INFINITY ? top - kAt : m + up;
+    if constexpr (F16) floor = fmaxf(floor, m - kFall);
+  }
+};
 
 // Partial results in a workspace: (m, l) of every row and part, then O.
 struct AttnParts {

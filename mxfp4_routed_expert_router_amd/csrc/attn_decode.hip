@@ -217,7 +217,8 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   f32x4 o[CT];
 #pragma unroll
   for (int i = 0; i < CT; ++i) o[i] = f32x4{0, 0, 0, 0};
-  float m = -INFINITY, l = 0.0f;
+  Reference<F16> ref;
+  float l = 0.0f;
   const float c = a.c;
   R k, v;
   RowScales<DP> sc_now;
@@ -258,8 +259,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
             lds_16(kXor ? (get_k ^ (st << 6)) + 16 * h * (2 * DP)
                         : lds0 + (16 * h + r) * (2 * DP) + (((4 * st + g) ^ swizzle_k<DP>(16 * h + r)) << 4)),
             qf[st], s[h]);
-    // m: reference of the exponents (base 2, scaled).  It rises only when some head's maximum passes it by more than 2^8.
-    const float base = m == -INFINITY ? 0.0f : m;
+    const float base = ref.m == -INFINITY ? 0.0f : ref.m;
     float top = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -271,11 +271,11 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
       }
     top = fmaxf(top, __shfl_xor(top, 16, kWave));
     top = fmaxf(top, __shfl_xor(top, 32, kWave));
-    if (__builtin_expect(wave_any((top > 8.0f) | ((m == -INFINITY) & (top > -INFINITY))), 0)) {
-      float up = m == -INFINITY ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
+    if (__builtin_expect(wave_any(ref.moves(top)), 0)) {
+      float up = ref.way(top);
       asm volatile("" : "+v"(up));  // (nothing of this rare block ahead of its branch)
-      const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up);  // (O and l are zero before the first key)
-      m = m == -INFINITY ? top : m + up;
+      const float f = ref.factor(up);
+      ref.move(top, up);
       l *= f;
 #pragma unroll
       for (int i = 0; i < CT; ++i) o[i] *= f;
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
   l += __shfl_xor(l, 16, kWave);
   l += __shfl_xor(l, 32, kWave);
   if (g == 0) {
-    stat[wave][0][r] = m;
+    stat[wave][0][r] = ref.m;
     stat[wave][1][r] = l;
   }
   __syncthreads();
@@ -343,7 +343,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves, PER_SIMD) void decode_kernel(Dec
 #pragma unroll
   for (int w = 0; w < W; ++w)
     sum += stat[w][0][r] == -INFINITY ? stat[w][1][r] : stat[w][1][r] * __builtin_amdgcn_exp2f(stat[w][0][r] - all);
-  const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - all);
+  const float f = ref.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(ref.m - all);
   // O of a wave as [16 heads][DP] fp32, in its tile's place: float 4-groups of a head's row take turns with the head
   float* ow = reinterpret_cast<float*>(tiles[wave]);
 #pragma unroll

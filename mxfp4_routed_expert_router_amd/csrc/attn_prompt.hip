@@ -223,8 +223,8 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
-  // m: reference of the exponents (base 2, scaled; at most 8 below the maximum), l: sum over this lane's keys
-  float m = -INFINITY, l = 0.0f;
+  Reference<F16> ref;
+  float l = 0.0f;  // sum over this lane's keys
   const float c = a.c;
 
   const auto v_frag = [&](uint32_t buf, int ks, int dt) {
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
       }
       wild = wave_any(std::max<uint16_t>(most[0], most[1]) >= (F16 ? 0x7C00 : 0x7F80));
     }
-    const float base = m == -INFINITY ? 0.0f : m;
+    const float base = ref.m == -INFINITY ? 0.0f : ref.m;
 #pragma unroll
     for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
@@ -293,12 +293,11 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[kt][r]);
     top = other_half_max(top);
-    // The reference rises only when some row's maximum passes it by more than 2^8: every exponential stays below that
-    if (__builtin_expect(wave_any((top > 8.0f) | ((m == -INFINITY) & (top > -INFINITY))), 0)) {
-      float up = m == -INFINITY ? (top == -INFINITY ? 0.0f : top) : fmaxf(top, 0.0f);
+    if (__builtin_expect(wave_any(ref.moves(top)), 0)) {
+      float up = ref.way(top);
       asm volatile("" : "+v"(up));  // (nothing of this rare block ahead of its branch)
-      const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(-up);  // (before the first key O and l are zero)
-      m = m == -INFINITY ? top : m + up;
+      const float f = ref.factor(up);
+      ref.move(top, up);
       l *= f;
 #pragma unroll
       for (int i = 0; i < DT; ++i) o[i] *= f;
@@ -418,7 +417,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
     const AttnParts w = attn_parts_dev(a.ws, (int64_t)a.Tq * a.Hq, a.parts);
     const int64_t at = orow * a.parts + blockIdx.y;
     if (half == 0) {
-      w.ml[2 * at] = m;
+      w.ml[2 * at] = ref.m;
       w.ml[2 * at + 1] = l;
     }
     if (n_tiles == 0) return;
@@ -451,7 +450,7 @@ __global__ __launch_bounds__(64 * NW, PER_SIMD) void prompt_kernel(PromptArgs a)
       const int d = 32 * dt + 8 * (q4 + half);
       if (mine && (EXACT || d < a.D)) st16(yp + d, w);
     }
-  if (mine && half == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
+  if (mine && half == 0 && a.lse) a.lse[orow] = l == 0.0f ? -INFINITY : (ref.m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 template <bool F16, int DP, int NW, int PER_SIMD>
