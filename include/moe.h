@@ -503,8 +503,9 @@ moe_status moe_linear(const void *x, moe_act_dtype x_dtype, int64_t x_row_stride
  *
  * moe_heads: [tokens][heads][head_dim] values; a head's values are contiguous, tokens and heads are token_stride and
  * head_stride values apart (both >= 0), so that q, k and v may be parts of one product's output, or 0 apart (broadcast).
- * Rows that are written are at least head_dim apart (else MOE_ERR_SHAPE; so are the rows of a cache that is written) and
- * lie over no input but where a call says so.  A HOST struct. */
+ * Rows that are written share no memory: in order of their strides, each stride of more than one step is at least the
+ * values that the smaller ones reach over, head_dim first (else MOE_ERR_SHAPE; so it is for a cache that is written and its
+ * scales).  They lie over no input but where a call says so.  A HOST struct. */
 #define MOE_MAX_HEADS 1024
 #define MOE_MAX_HEAD_DIM 256   /* a multiple of 8 */
 typedef struct {

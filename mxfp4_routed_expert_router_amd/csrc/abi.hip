@@ -837,10 +837,26 @@ moe_status check_heads(const moe_heads& h, int unit) {
     return MOE_ERR_ALIGN;
   return MOE_OK;
 }
-// Rows that are written: of `n` along a stride, no two may be the same (broadcast) or half over each other.
-inline bool overlaps(int64_t n, int64_t stride, int64_t values) { return n > 1 && stride < values; }
+// Rows of `values` values that are written, along dimensions of a count and a stride: in order of their strides, each has
+// to step over all that lies below it, or two rows share memory (token t's head h + 1 is token t + 1's head h, say).  That
+// refuses a few layouts of interlocking rows that would not, which no tensor has.
+struct Dim {
+  int64_t n, stride;
+};
+template <size_t N>
+bool overlaps(Dim (&&dims)[N], int64_t values) {
+  std::sort(dims, dims + N, [](const Dim& x, const Dim& y) { return x.stride < y.stride; });
+  int64_t reach = values;
+  for (const Dim& d : dims) {
+    if (d.n <= 1) continue;
+    if (d.stride < reach) return true;
+    // (strides end at kMostStride, so nothing steps over more than that)
+    reach = d.n - 1 > kMostStride / d.stride ? kMostStride + 1 : (d.n - 1) * d.stride + reach;
+  }
+  return false;
+}
 inline bool overlaps(const moe_heads& h, int T, int n_heads, int head_dim) {
-  return overlaps(T, h.token_stride, head_dim) || overlaps(n_heads, h.head_stride, head_dim);
+  return overlaps({{T, h.token_stride}, {n_heads, h.head_stride}}, head_dim);
 }
 moe_status check_cache(const moe_kv_cache& c) {
   if (c.fmt != MOE_KV_BF16 && c.fmt != MOE_KV_FP16 && c.fmt != MOE_KV_MXFP8) return MOE_ERR_DTYPE;
@@ -933,8 +949,7 @@ moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T,
     if (st != MOE_OK) return st;
     if (cache->n_kv_heads != n_kv_heads || cache->head_dim != head_dim) return MOE_ERR_SHAPE;
     const auto rows = [&](int64_t page, int64_t head, int64_t token, int64_t values) {
-      return overlaps(cache->n_pages, page, values) || overlaps(n_kv_heads, head, values) ||
-             overlaps(cache->page_size, token, values);
+      return overlaps({{cache->n_pages, page}, {n_kv_heads, head}, {cache->page_size, token}}, values);
     };
     if (rows(cache->page_stride, cache->head_stride, cache->token_stride, head_dim) ||
         (cache->fmt == MOE_KV_MXFP8 &&

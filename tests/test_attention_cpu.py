@@ -243,3 +243,57 @@ def test_reference_forms():
     c = m.KvCache(torch.randn(3, 1, 4, 8).bfloat16(), torch.randn(3, 1, 4, 8).bfloat16())
     kk, vv, there = ref.cache_rows(c, pages[0], 9)
     assert torch.equal(kk[5], c.tensors[0][0, :, 1].double()) and there.tolist() == [True] * 8 + [False]
+
+
+def test_outputs_whose_strides_do_not_nest():
+    """Each stride alone steps over a row, but two of them together come back to the same memory: (t, h + 1) is (t + 1, h)."""
+    L = m.lib()
+    out = P + 0x10000
+
+    def rows_refused(ts, hs, T=8, n=4):
+        y, x = heads(out, ts=ts, hs=hs), heads(ts=4096)
+        got = {L.moe_attention_prompt(ref_(x), ref_(x), ref_(x), P, P, 2, T, 8, n, 2, 64, 0.125, 1, 0, ref_(y), None, None, 0,
+                                      None),
+               L.moe_attention_decode(ref_(x), T, n, ref_(cache_desc(m.MOE_KV_BF16)), P, 10, 10, P, 16, 0.125, 0, ref_(y), None,
+                                      None, 0, None)}
+        for at in range(3):
+            outs = [ref_(y if i == at else heads(out + (1 << 20) * (i + 1), ts=4096)) for i in range(3)]
+            got.add(L.moe_rope_cache(None, None, T, n, n, 64, ref_(x), ref_(x), ref_(x), *outs, None, None, None))
+        return got == {SHAPE}
+
+    for ts, hs in ((64, 64), (192, 64), (64, 448), (128, 128), (248, 64), (72, 64), (64, 504)):
+        assert rows_refused(ts, hs), (ts, hs)
+
+    def cache_refused(fmt, **over):
+        k = heads(ts=4096)
+        return L.moe_rope_cache(None, None, 4, 0, 2, 64, None, ref_(k), ref_(k), None, None, None, ref_(cache_desc(fmt, **over)),
+                                P, None) == SHAPE
+
+    for fmt in (m.MOE_KV_BF16, m.MOE_KV_FP16, m.MOE_KV_MXFP8):
+        # ten pages of 16 tokens and 2 heads of 64
+        for over in (dict(page_stride=1024), dict(page_stride=2032), dict(head_stride=64), dict(head_stride=1008),
+                     dict(token_stride=128), dict(token_stride=1024), dict(page_stride=64), dict(token_stride=2048, head_stride=64),
+                     dict(page_stride=1 << 40, head_stride=1 << 40), dict(head_stride=1 << 40, token_stride=1 << 40)):
+            assert cache_refused(fmt, **over), over
+    for over in (dict(s_page_stride=32), dict(s_page_stride=62), dict(s_head_stride=2), dict(s_token_stride=4),
+                 dict(s_head_stride=2, s_token_stride=2)):
+        assert cache_refused(m.MOE_KV_MXFP8, **over), over
+
+
+def test_nesting_against_all_rows():
+    """What passes the check lies apart by the list of all rows.  (Passing calls end at their missing workspace.)"""
+    L = m.lib()
+    Tq, Tk, n, D = 3, 50000, 4, 8
+    assert L.moe_attention_prompt_workspace_bytes(Tq, Tk, 1, n, 2, D) > 0
+    x = heads(ts=64, hs=8)
+    some = 0
+    for ts in range(0, 121, 8):
+        for hs in range(0, 121, 8):
+            st = L.moe_attention_prompt(ref_(x), ref_(x), ref_(x), P, P, 1, Tq, Tk, n, 2, D, 0.125, 1, 0,
+                                        ref_(heads(P + 0x100000, ts=ts, hs=hs)), None, None, 0, None)
+            nested = (ts >= (n - 1) * hs + D and hs >= D) or (hs >= (Tq - 1) * ts + D and ts >= D)
+            assert st == (WORKSPACE if nested else SHAPE), (ts, hs, st)
+            at = sorted(i * ts + j * hs for i in range(Tq) for j in range(n))
+            assert not nested or all(b - a >= D for a, b in zip(at, at[1:])), (ts, hs)
+            some += nested
+    assert some > 50
