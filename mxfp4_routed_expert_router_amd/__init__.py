@@ -914,7 +914,7 @@ class KvCache:
             raise ValueError("KvCache: 16-bit values take no scales")
         self.act = torch.float16 if fmt == MOE_KV_FP16 else torch.bfloat16  # type of q and y
         self.at = ctypes.addressof(self.c)
-        self._need = {}  # workspace bytes by (B, heads, max_len)
+        self._need = (None, 0)  # the last (B, heads, max_len) asked for and its workspace bytes
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt: str = "bf16", device="cuda"):
@@ -1015,10 +1015,10 @@ def moe_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
 
 def moe_attention_decode_workspace_bytes(B: int, n_q_heads: int, cache: KvCache, max_len: int) -> int:
     key = (B, n_q_heads, max_len)
-    need = cache._need.get(key)
-    if need is None:
-        need = cache._need[key] = lib().moe_attention_decode_workspace_bytes(B, n_q_heads, cache.n_kv_heads,
-                                                                             cache.head_dim, max_len)
+    last, need = cache._need
+    if last != key:
+        need = lib().moe_attention_decode_workspace_bytes(B, n_q_heads, cache.n_kv_heads, cache.head_dim, max_len)
+        cache._need = (key, need)
     return need
 
 

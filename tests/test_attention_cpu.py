@@ -297,3 +297,18 @@ def test_nesting_against_all_rows():
             assert not nested or all(b - a >= D for a, b in zip(at, at[1:])), (ts, hs)
             some += nested
     assert some > 50
+
+
+def test_workspace_queries_are_not_kept_without_end():
+    """A server that passes each step's longest length asks for a new size every step."""
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    cache = m.KvCache(bf(4, 2, 16, 64), bf(4, 2, 16, 64))
+    L = m.lib()
+    sizes = set()
+    for n in list(range(1, 5000)) + [7, 4999]:
+        got = m.moe_attention_decode_workspace_bytes(3, 4, cache, n)
+        assert got == L.moe_attention_decode_workspace_bytes(3, 4, 2, 64, n)
+        sizes.add(got)
+    assert len(sizes) > 10
+    held = sum(len(v) for v in vars(cache).values() if isinstance(v, (dict, list, set)))
+    assert held <= 64, held
