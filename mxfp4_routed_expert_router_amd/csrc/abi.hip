@@ -1084,12 +1084,10 @@ moe_status moe_attention_decode(const moe_heads* q, int B, int n_q_heads, const 
   a.Hkv = cache->n_kv_heads;
   a.D = cache->head_dim;
   a.G = n_q_heads / cache->n_kv_heads;
-  a.f16 = dt == MOE_DT_FP16;
   a.table = page_table;
   a.table_stride = table_stride;
   a.lens = lens;
   a.max_len = max_len;
-  a.width = table_width;
   a.window = window;
   a.n_pages = cache->n_pages;
   a.fmt = cache->fmt;

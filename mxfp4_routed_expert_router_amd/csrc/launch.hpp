@@ -214,11 +214,11 @@ struct DecodeArgs {
   uint16_t* y;
   float* lse;                 // [B][Hq] or NULL
   int64_t q_ts, q_hs, y_ts, y_hs;
-  int B, Hq, Hkv, D, G, f16;
-  const int32_t* table;       // [B] rows of `width` page numbers
+  int B, Hq, Hkv, D, G;
+  const int32_t* table;       // [B] rows of page numbers
   int64_t table_stride;
   const int32_t* lens;
-  int max_len, width, window, n_pages, fmt;
+  int max_len, window, n_pages, fmt;
   const void *cache_k, *cache_v;
   const uint8_t *scale_k, *scale_v;
   int64_t c_page, c_head, c_token, s_page, s_head, s_token;
