@@ -860,6 +860,11 @@ def _ints(what: str, t: torch.Tensor, shape, index: int) -> int:
                      f"{tuple(t.shape)} on {t.device}")
 
 
+def _too_large(what: str, **sizes):
+    """(ctypes would pass the lower 32 bits on.)"""
+    raise ValueError(f"{what}: {', '.join(f'{k} = {v}' for k, v in sizes.items() if v >> 31 > 0)} does not fit 32 bits")
+
+
 class Rope:
     """Cosines and sines of the positions' angles, fp32 [n_positions][rotary_dim / 2], and how values pair up
     (moe_rope): "halves" (i, i + rotary_dim / 2) or "neighbours" (2i, 2i + 1)."""
@@ -940,6 +945,8 @@ def moe_rope_cache(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Opti
         raise ValueError("moe_rope_cache: needs q or k")
     gpu = _gpu(x)
     T, _, D = x.shape
+    if T >> 31:
+        _too_large("moe_rope_cache", T=T)
     nq = 0 if q is None else q.shape[1]
     nkv = 0 if k is None else k.shape[1]
     if out is None:
@@ -993,6 +1000,8 @@ def moe_attention_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q
     Tq, nq, D = q.shape
     Tk, nkv = k.shape[:2]
     n = cu_q.shape[0] - 1
+    if (Tq | Tk | window) >> 31 > 0:
+        _too_large("moe_attention_prompt", Tq=Tq, Tk=Tk, window=window)
     qh = _heads("moe_attention_prompt: q", q, (Tq, nq, D), gpu)
     kh = _heads("moe_attention_prompt: k", k, (Tk, nkv, D), gpu)
     vh = _heads("moe_attention_prompt: v", v, (Tk, nkv, D), gpu)
@@ -1042,6 +1051,8 @@ def moe_attention_decode(q: torch.Tensor, cache: KvCache, page_table: torch.Tens
     stride = _rows("moe_attention_decode: page_table", page_table, (B, width), gpu)
     if max_len is None:
         max_len = width * cache.page_size
+    if (B | max_len | window) >> 31 > 0:
+        _too_large("moe_attention_decode", B=B, max_len=max_len, window=window)
     ws = workspace
     if ws is None:
         need = moe_attention_decode_workspace_bytes(B, nq, cache, max_len)

@@ -159,3 +159,31 @@ def test_decode_key_scale_codes(code):
     q = torch.zeros(1, 4, D, dtype=torch.bfloat16, device=DEV)
     q[:, :, 3] = 2.0 ** max(-120, min(120, 128 - code))
     run_decode(q, cache, table, [n], scale=0.25, what=f"key scale {code}")
+
+
+def test_numbers_beyond_32_bits():
+    """The C calls take 32-bit numbers: a larger one is refused, not taken without its upper half (2^32 + 5 as 5)."""
+    cache, table = make_cache([40], 16, 2, 64, "bf16", 1)
+    q = queries(1, 4, 64, torch.bfloat16, 2)
+    t, n = table.to(DEV), torch.tensor([40], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    k = queries(1, 2, 64, torch.bfloat16, 3)
+    for large in (1 << 31, 1 << 32, (1 << 32) + 5, 1 << 40):
+        for call in (lambda: moe.moe_attention_decode(q, cache, t, n, max_len=large),
+                     lambda: moe.moe_attention_decode(q, cache, t, n, window=large),
+                     lambda: moe.moe_attention_prompt(q, k, k, cu, window=large)):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+    wide = torch.zeros(1, 1 << 24, dtype=torch.int32, device=DEV)  # 2^24 pages of 256 tokens: max_len would be 0
+    big = moe.KvCache.empty(1, 256, 2, 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.moe_attention_decode(q, big, wide, n)
+    few = torch.zeros(1, 1, 8, dtype=torch.bfloat16, device=DEV)
+    many = few.expand((1 << 32) + 1, 1, 8)
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.moe_rope_cache(many, None, None, out=(many, None, None))
+    with pytest.raises(ValueError, match="32 bits"):
+        moe.moe_attention_prompt(few, many, many, cu)
+    for bad in (dict(window=-1), dict(max_len=-1)):
+        with pytest.raises(moe.MoEError):
+            moe.moe_attention_decode(q, cache, t, n, **bad)
