@@ -906,7 +906,7 @@ moe_status moe_rope_cache(const moe_rope* rope, const int32_t* positions, int T,
       n_q_heads + n_kv_heads < 1 || head_dim < 8 || head_dim > MOE_MAX_HEAD_DIM || head_dim % 8 != 0)
     return MOE_ERR_SHAPE;
   if ((int64_t)T * (n_q_heads + 2 * n_kv_heads) > (int64_t)1 << 27) return MOE_ERR_SHAPE;
-  if ((n_q_heads > 0 && (!q || !q_out)) || (n_kv_heads > 0 && !k) || ((v_out || cache) && !v)) return MOE_ERR_NULL;
+  if ((n_q_heads > 0 && (!q || !q_out)) || (n_kv_heads > 0 && (!k || ((v_out || cache) && !v)))) return MOE_ERR_NULL;
   if (n_kv_heads > 0 && !k_out && !v_out && !cache) return MOE_ERR_NULL;
   if ((cache != nullptr) != (slots != nullptr)) return MOE_ERR_NULL;
   if ((rope != nullptr) != (positions != nullptr)) return MOE_ERR_NULL;

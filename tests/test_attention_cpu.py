@@ -312,3 +312,13 @@ def test_workspace_queries_are_not_kept_without_end():
     assert len(sizes) > 10
     held = sum(len(v) for v in vars(cache).values() if isinstance(v, (dict, list, set)))
     assert held <= 64, held
+
+
+def test_rope_without_key_value_heads_uses_none_of_their_pointers():
+    """n_kv_heads 0: k, v and their outputs do not count, whatever they are.  (The calls end at the misaligned table.)"""
+    L = m.lib()
+    bad = m.moe_rope(P + 2, P + 4096, 100, 64, 0)
+    for k, v, ko, vo in ((None, None, None, heads()), (None, None, heads(), heads()), (heads(None), None, None, heads(None)),
+                         (None, heads(dt=7), None, None)):
+        assert L.moe_rope_cache(ref_(bad), P, 4, 4, 0, 64, ref_(heads()), ref_(k), ref_(v), ref_(heads(P + 0x10000)), ref_(ko),
+                                ref_(vo), None, None, None) == ALIGN
