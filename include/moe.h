@@ -563,11 +563,11 @@ moe_status moe_rope_cache(const moe_rope *rope, const int32_t *positions, int T,
  * nk keys, query i stands at key position p = i + nk - nq and sees keys j with j <= p (causal) and j > p - window
  * (window > 0; causal only):
  *   y[i,h] = sum_j softmax_j(scale * q[i,h] . k[j,h/G]) v[j,h/G],  lse[i,h] = ln sum_j exp(scale * q[i,h] . k[j,h/G])
- * (fp32 sums; the exponentials are rounded to the 16-bit type before their product with v; one rounding of y).  In fp16 a
- * weight below 2^-14 of the largest of its 64 keys is off by up to 2^-25 of that one (below 2^-21 and by 2^-32 among the
- * keys of the row's largest).  A row
- * that sees no key, or only keys of score -inf, gets y = 0 and lse = -inf.  A NaN or infinity in a key or value reaches
- * the rows that see it and no other.  Rows of y outside the sequences are not touched.
+ * (fp32 sums; the exponentials are rounded to the 16-bit type before their product with v, not in their sum, which moves y by
+ * up to half a step of the mean magnitude of v; one rounding of y).  In fp16 a weight below 2^-14 of the largest of its 64 keys
+ * is off by up to 2^-25 of that one (among the keys of the row's largest: below 2^-21, by up to 2^-32).  A row that sees no
+ * key, or only keys of score -inf, gets y = 0 and lse = -inf.  A NaN or infinity in a key or value reaches the rows that see
+ * it and no other.  Rows of y outside the sequences are not touched.
  *   q, y  [Tq][n_q_heads][head_dim], k, v [Tk][n_kv_heads][head_dim]: one type, bf16 or fp16; 16-byte aligned, strides
  *         multiples of 8 values
  *   lse   [Tq][n_q_heads] fp32, or NULL
@@ -585,7 +585,8 @@ moe_status moe_attention_prompt(const moe_heads *q, const moe_heads *k, const mo
  * them, or all (window 0):
  *   y[b,h], lse[b,h] as for moe_attention_prompt (fp32 sums; the exponentials are two 16-bit parts, so an infinite
  *   value that is seen may give NaN; one rounding of y).  In fp16 the low part of a weight is off by up to 2^-25 of the
- *   largest weight of its 32 keys (2^-32 among the keys of the row's largest).
+ *   largest weight of its 32 keys (2^-32 among the keys of the row's largest).  MXFP8 values are taken as bf16 ones: exact
+ *   above 2^-126, multiples of 2^-133 below, infinities from 2^128 on.
  * No keys: y = 0, lse = -inf.  Tokens on a page number outside [0, n_pages) are left out.  Rows may share pages and table
  * rows (several newest tokens of one sequence: one row each, with rising lens).
  *   q, y        [B][n_q_heads][head_dim] bf16 (MOE_KV_BF16, MOE_KV_MXFP8) or fp16 (MOE_KV_FP16), 16-byte aligned, strides

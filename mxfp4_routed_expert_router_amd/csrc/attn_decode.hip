@@ -4,11 +4,11 @@
 // take 32 keys at a time, each with a running maximum and sum of its own, and join at the end through LDS.  S^T = K Q^T
 // puts a head into a column (lane & 15), so maxima, sums and rescaling stay in a lane but for two exchanges, and P^T is
 // the right operand of O^T = V^T P^T as it stands, rounded to a high and a low 16-bit part: the cache's bytes bound the
-// kernel, so the second product costs nothing and only the output is rounded.
+// kernel, so the second product costs nothing and only the output is rounded (in fp16 as far as its exponents reach).
 //
 // Consecutive lanes read consecutive 16 bytes of a token's row, whole 128-byte lines a load and past the caches: in MFMA
 // layout at once (64 bytes of sixteen rows a load) 176 sequences of up to 4096 tokens take 266 us, so 215 (5.6 TB/s; reading
-// alone reaches 7.17).  The tile then
+// alone reaches 7.17; on pages of 16 tokens, with an address to a key, the same within 3%, in MXFP8 5% more).  The tile then
 // turns through a part of LDS that is the wave's own.  The next tile's K and V are on their way meanwhile (MXFP8 from heads of
 // 128 on: one of them).
 //

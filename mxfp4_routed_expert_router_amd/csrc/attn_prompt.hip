@@ -10,7 +10,10 @@
 // Operations bound it: 4 D per row and key on the matrix cores, and about as much time on the vector ALU for the
 // exponentials, which run beside them.  16384 tokens, 64 heads of 128 on 8: 4.0 ms, 1.1 PFLOP/s, the matrix cores busy 61%
 // of the cycles at 1.72 GHz; the card's power holds it there (with 50% the clock was 1.97 GHz).  P is rounded to 16 bits
-// (half a step, as the output is; its errors are random and average out over the keys); maxima, sums and O are fp32.
+// (half a step, as the output is); maxima, sums and O are fp32.  The sum is of the unrounded exponentials, which the log sum
+// needs: errors that differ from key to key average out, but where many keys of one score carry a row they all err alike, and
+// y by as much, up to that half step.  A second sum, of the rounded ones, would take that out for 5% more time (16384 tokens:
+// 3835 -> 4035 us; heads of 256, which have no registers left for it, 186 -> 232).
 #include <limits.h>
 
 #include <algorithm>
